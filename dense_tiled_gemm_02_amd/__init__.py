@@ -25,6 +25,10 @@ GEMM_ERR_HIP = 3
 GEMM_ERR_WORKSPACE = 4
 GEMM_XCD_ON = 1
 GEMM_XCD_OFF = 2
+GEMM_GROUPED_ROWS = 0     # D (R x Q) = A (R x P) x B[group of the row] (P x Q)
+GEMM_GROUPED_REDUCE = 1   # D[group] (P x Q) = A_g^T x B_g over the group's rows
+GEMM_GROUPED_OUT_SAME = 0
+GEMM_GROUPED_OUT_F32 = 1
 GEMM_STATIC_SCRATCH_BYTES = 24 << 20   # include/gemm.h: the workspace gemm_run_static provides
 KERNEL_TILE = 1
 KERNEL_SKINNY = 2
@@ -55,6 +59,20 @@ class gemm_config(ctypes.Structure):
 class gemm_device_info(ctypes.Structure):
     _fields_ = [("arch", _i32), ("cu_count", _i32), ("xcd_count", _i32), ("clock_khz", _i32),
                 ("lds_per_cu", _i64), ("lds_per_wg", _i64), ("wave_size", _i32)]
+
+
+class gemm_grouped_problem(ctypes.Structure):
+    _fields_ = [("groups", _i64), ("R", _i64), ("P", _i64), ("Q", _i64),
+                ("sa_r", _i64), ("sa_p", _i64), ("sb_g", _i64), ("sb_r", _i64), ("sb_q", _i64),
+                ("sd_g", _i64), ("sd_r", _i64),
+                ("dtype", ctypes.c_int), ("kind", ctypes.c_int), ("out", ctypes.c_int), ("accumulate", _i32)]
+
+
+class gemm_w4_problem(ctypes.Structure):
+    _fields_ = [("M", _i64), ("N", _i64), ("K", _i64), ("group", _i64), ("experts", _i64),
+                ("sx", _i64), ("sy", _i64), ("sw_n", _i64), ("sw_e", _i64), ("ss_n", _i64), ("ss_e", _i64),
+                ("sz_n", _i64), ("sz_e", _i64),
+                ("dtype", ctypes.c_int), ("has_zeros", _i32), ("id_bytes", _i32)]
 
 
 class GemmError(RuntimeError):
@@ -90,6 +108,25 @@ SIGNATURES = [
      [_i64, _i64, _i64, _i32, _i32, ctypes.POINTER(_i64), ctypes.POINTER(_i64)]),
     ("gemm_streamk_pieces", ctypes.c_int,
      [_i32, _i32, _i32, _i32, ctypes.POINTER(_i32), _i32, ctypes.POINTER(_i32)]),
+    ("gemm_grouped_plan_create", ctypes.c_int,
+     [ctypes.POINTER(gemm_grouped_problem), ctypes.c_int, ctypes.POINTER(gemm_config), ctypes.POINTER(_p)]),
+    ("gemm_grouped_plan_create_for", ctypes.c_int,
+     [ctypes.POINTER(gemm_grouped_problem), ctypes.POINTER(gemm_device_info), ctypes.POINTER(gemm_config),
+      ctypes.POINTER(_p)]),
+    ("gemm_grouped_plan_destroy", None, [_p]),
+    ("gemm_grouped_plan_config", ctypes.c_int, [_p, ctypes.POINTER(gemm_config)]),
+    ("gemm_grouped_plan_launch", ctypes.c_int,
+     [_p, ctypes.POINTER(_i64), ctypes.POINTER(_i32), ctypes.POINTER(_i64)]),
+    ("gemm_grouped_plan_describe", ctypes.c_int, [_p, ctypes.c_char_p, ctypes.c_size_t]),
+    ("gemm_grouped_run", ctypes.c_int, [_p, _p, _p, _p, _p, _p]),
+    ("gemm_group_rows", ctypes.c_int, [_p, _i32, _i64, _i64, _p, _p, _p, ctypes.c_size_t, _p]),
+    ("gemm_group_rows_workspace", ctypes.c_int, [_i64, _i64, ctypes.POINTER(ctypes.c_size_t)]),
+    ("gemm_w4_plan_create", ctypes.c_int, [ctypes.POINTER(gemm_w4_problem), ctypes.c_int, ctypes.POINTER(_p)]),
+    ("gemm_w4_plan_create_for", ctypes.c_int,
+     [ctypes.POINTER(gemm_w4_problem), ctypes.POINTER(gemm_device_info), ctypes.POINTER(_p)]),
+    ("gemm_w4_plan_destroy", None, [_p]),
+    ("gemm_w4_plan_describe", ctypes.c_int, [_p, ctypes.c_char_p, ctypes.c_size_t]),
+    ("gemm_w4_run", ctypes.c_int, [_p, _p, _p, _p, _p, _p, _p, _p]),
     ("gemm_status_string", ctypes.c_char_p, [ctypes.c_int]),
     ("gemm_last_error", ctypes.c_char_p, []),
 ]

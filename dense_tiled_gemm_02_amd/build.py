@@ -29,7 +29,9 @@ ARCH = "gfx950"
 SOURCES = ["api.cpp", "api_mx.cpp", "gemm_tile.hip", "gemm_dma.hip", "gemm_dma_more.hip", "gemm_dma_layouts.hip", "gemm_dma_sk.hip",
            "gemm_mx.hip", "gemm_mx_pairs.hip",
            "gemm_skinny.hip", "gemm_static.hip", "gemm_i8.hip",
-           "gemm_mx_direct.hip"]
+           "gemm_mx_direct.hip",
+           "api_grouped.cpp", "gemm_grouped_rows.hip", "gemm_grouped_reduce.hip", "gemm_grouped_any.hip",
+           "group_rows.hip", "api_w4.cpp", "gemm_w4.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 COMMON = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=" + ARCH,

@@ -137,9 +137,10 @@ __device__ __forceinline__ Work slice_work(const KArgs& p) {
 // XCH: the K-slice exchange is compiled for tiles of more than 64
 // accumulators per lane too (the stream-K variants).  NTB: B is loaded
 // non-temporal (the variants for a grid of one row of tiles, where each byte
-// of B is read by one workgroup per K slice).
+// of B is read by one workgroup per K slice).  O32: C and D are fp32 (the
+// weight gradients of the products grouped by expert).
 template <int BM, int BN, int BK, int WM, int WN, int MF, int ST, int EL, bool TA, bool TB, bool XCH = false,
-          bool NTB = false>
+          bool NTB = false, bool O32 = false>
 __device__ __forceinline__ void dma_tile(const KArgs& p, const Work& wk) {
     constexpr bool BF16 = EL == kElBF16;
     constexpr bool I8 = EL == kElI8;
@@ -161,7 +162,7 @@ __device__ __forceinline__ void dma_tile(const KArgs& p, const Work& wk) {
     // accumulators per lane; above 128 (one wave per SIMD holding a
     // 128 x 128 wave tile) they live in AGPRs, placed there explicitly
     constexpr bool AGPR = FM * FN * AccT<MF>::regs > 128;
-    static_assert(!(I8 && AGPR), "int8 tiles keep their accumulators in VGPRs");
+    static_assert(!((I8 || O32) && AGPR), "tiles with 32-bit output keep their accumulators in VGPRs");
 
     __shared__ __attribute__((aligned(1024))) uint16_t smem[ST * (SA + SB)];
 
@@ -617,18 +618,18 @@ __device__ __forceinline__ void dma_tile(const KArgs& p, const Work& wk) {
     // 0..3; 32x32x16: run q at columns 8 q + 4 (l / 32) + 0..3).
     constexpr int G = AccT<MF>::regs / 4;
 
-    if constexpr (I8) {
-        // int32 results: the tile is staged through LDS in P8 passes of BM / P8
-        // rows (16-byte chunks of 4 values at chunk position c ^ (r mod 16) of
-        // their row), then each thread adds C to a 4-value row chunk and
-        // writes it as one 16-byte store.  Integer sums wrap modulo 2^32, as
-        // the instruction's accumulator does.
+    if constexpr (I8 || O32) {
+        // 32-bit results (int32, or fp32 with O32): the tile is staged through
+        // LDS in P8 passes of BM / P8 rows (16-byte chunks of 4 values at
+        // chunk position c ^ (r mod 16) of their row), then each thread adds C
+        // to a 4-value row chunk and writes it as one 16-byte store.  Integer
+        // sums wrap modulo 2^32, as the instruction's accumulator does.
         constexpr int LDSB = ST * (SA + SB) * 2;
         constexpr int P8 = (BM * BN * 4 <= LDSB)                       ? 1
                            : (WM % 2 == 0 && BM * BN * 2 <= LDSB)     ? 2
                            : (WM % 4 == 0 && BM * BN <= LDSB)         ? 4
                                                                       : 0;
-        static_assert(P8 > 0, "the int32 tile must fit the LDS in at most 4 passes");
+        static_assert(P8 > 0, "the 32-bit tile must fit the LDS in at most 4 passes");
         constexpr int PR = BM / P8, WPP = WM / P8, C4 = BN / 4, NT = 64 * NW;
         static_assert((PR * C4) % NT == 0 && C4 >= 16, "whole rounds of 4-value chunks");
         typedef uint32_t v4u __attribute__((ext_vector_type(4)));
@@ -636,6 +637,10 @@ __device__ __forceinline__ void dma_tile(const KArgs& p, const Work& wk) {
         uint32_t* const D32 = reinterpret_cast<uint32_t*>(p.D);
         const uint32_t* const C32 = reinterpret_cast<const uint32_t*>(p.C);
         const bool has_c = p.has_c != 0;
+        auto plus = [](uint32_t x, uint32_t c) -> uint32_t {
+            if constexpr (O32) return __float_as_uint(__uint_as_float(x) + __uint_as_float(c));
+            else return x + c;
+        };
         const bool vec4 = (p.ldd % 4 == 0) && (reinterpret_cast<uintptr_t>(p.D) % 16 == 0) &&
                           (!has_c || ((p.ldc % 4 == 0) && (reinterpret_cast<uintptr_t>(p.C) % 16 == 0)));
 #pragma unroll
@@ -667,11 +672,15 @@ __device__ __forceinline__ void dma_tile(const KArgs& p, const Work& wk) {
                     uint32_t* d = D32 + static_cast<int64_t>(gr) * p.ldd + gc;
                     const uint32_t* c = has_c ? C32 + static_cast<int64_t>(gr) * p.ldc + gc : nullptr;
                     if (vec4 && gc + 4 <= N) {
-                        if (has_c) v += *reinterpret_cast<const v4u*>(c);
+                        if (has_c) {
+                            const v4u cv = *reinterpret_cast<const v4u*>(c);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[e] = plus(v[e], cv[e]);
+                        }
                         typedef unsigned int nt_u32x4 __attribute__((ext_vector_type(4)));
                         __builtin_nontemporal_store(__builtin_bit_cast(nt_u32x4, v), reinterpret_cast<nt_u32x4*>(d));
                     } else {
-                        for (int e = 0; e < 4 && gc + e < N; ++e) d[e] = v[e] + (has_c ? c[e] : 0u);
+                        for (int e = 0; e < 4 && gc + e < N; ++e) d[e] = has_c ? plus(v[e], c[e]) : v[e];
                     }
                 }
             }

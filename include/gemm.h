@@ -275,6 +275,129 @@ gemm_status gemm_tile_of_workgroup(int64_t wg, int64_t num_pid_m, int64_t num_pi
 gemm_status gemm_streamk_pieces(int32_t tiles, int32_t k_steps, int32_t workgroups, int32_t wg,
                                 int32_t* out, int32_t max_pieces, int32_t* count);
 
+/* ---- Products grouped by an offset table (the experts of a mixture-of-experts
+ * layer).
+ *
+ * The R rows of an operand are sorted by group; a device table of groups + 1
+ * int32 offsets says that group g owns rows [offsets[g], offsets[g + 1]).  The
+ * host never reads it: no synchronization, and a captured graph replays with
+ * other tables.  offsets must not decrease; bounds are clamped to [0, R].  A
+ * group may be empty, and rows before offsets[0] or from offsets[groups] on
+ * (capacity padding) belong to no group.  A table that decreases may leave
+ * outputs unwritten; nothing outside the operands is read or written.
+ *
+ *  GEMM_GROUPED_ROWS    D (R x Q) = A (R x P) x B[g] (P x Q), g the row's group;
+ *                       rows of no group are written as zeros.  With the
+ *                       transposed strides of B this is the input gradient.
+ *  GEMM_GROUPED_REDUCE  D[g] (P x Q) = sum over the group's rows i of
+ *                       A[i, :]^T x B[i, :], A (R x P), B (R x Q): the gradient
+ *                       of B[g] above.  An empty group gives zeros.  With
+ *                       accumulate = 1 the sum is added to D instead, once in
+ *                       fp32, and rounded to D's type.
+ *
+ * fp16 or bf16 operands, fp32 sums, one rounding to D's type (the operands'
+ * or, for GEMM_GROUPED_REDUCE, fp32).  The accuracy contract of the dense
+ * product holds with the sum over the row's P or the group's rows.  Bitwise
+ * reproducible for a fixed plan and table.
+ *
+ * Any strides >= 0 of A and B run; the direct-to-LDS tiles take A and B with a
+ * contiguous index (A along P; B along Q, or along P for GEMM_GROUPED_ROWS)
+ * whose extent and whose other strides are multiples of 8, with 16-byte
+ * aligned bases; everything else runs on an element-wise tile. */
+typedef enum gemm_grouped_kind { GEMM_GROUPED_ROWS = 0, GEMM_GROUPED_REDUCE = 1 } gemm_grouped_kind;
+
+typedef enum gemm_grouped_out {
+    GEMM_GROUPED_OUT_SAME = 0,  /* D of the operands' type */
+    GEMM_GROUPED_OUT_F32 = 1    /* fp32 D (GEMM_GROUPED_REDUCE only) */
+} gemm_grouped_out;
+
+/* Strides in elements; D's column stride is 1.  At most 65535 groups. */
+typedef struct gemm_grouped_problem {
+    int64_t groups, R, P, Q;
+    int64_t sa_r, sa_p;         /* A: element (i, p) at A[i*sa_r + p*sa_p] */
+    int64_t sb_g, sb_r, sb_q;   /* B: (g, p, q) at B[g*sb_g + p*sb_r + q*sb_q] (rows),
+                                   (i, q) at B[i*sb_r + q*sb_q] (reduce; sb_g unused) */
+    int64_t sd_g, sd_r;         /* D: (i, q) at D[i*sd_r + q] (rows; sd_g unused),
+                                   (g, p, q) at D[g*sd_g + p*sd_r + q] (reduce) */
+    gemm_dtype dtype;           /* GEMM_F16 or GEMM_BF16 */
+    gemm_grouped_kind kind;
+    gemm_grouped_out out;
+    int32_t accumulate;         /* 1 (reduce only): D += the sum */
+} gemm_grouped_problem;
+
+typedef struct gemm_grouped_plan gemm_grouped_plan;   /* opaque, immutable after creation */
+
+/* As gemm_plan_create / gemm_plan_create_for.  A forced configuration's bm,
+ * bn, stages, mfma, waves_m, waves_n, bk select a compiled tile, group_m and
+ * xcd_remap the tile order; splitk must be 0 or 1 and kernel 0. */
+gemm_status gemm_grouped_plan_create(const gemm_grouped_problem* prob, int device, const gemm_config* force,
+                                     gemm_grouped_plan** out);
+gemm_status gemm_grouped_plan_create_for(const gemm_grouped_problem* prob, const gemm_device_info* info,
+                                         const gemm_config* force, gemm_grouped_plan** out);
+void gemm_grouped_plan_destroy(gemm_grouped_plan* plan);
+gemm_status gemm_grouped_plan_config(const gemm_grouped_plan* plan, gemm_config* out);
+
+/* Launch geometry; for GEMM_GROUPED_ROWS the grid covers the most tiles any
+ * table can need, and workgroups past the actual number leave at once. */
+gemm_status gemm_grouped_plan_launch(const gemm_grouped_plan* plan, int64_t* grid, int32_t* threads,
+                                     int64_t* lds_bytes);
+gemm_status gemm_grouped_plan_describe(const gemm_grouped_plan* plan, char* buf, size_t len);
+
+/* Enqueue the product on `stream`.  offsets: device, groups + 1 int32.  D may
+ * overlap neither A, B nor offsets.  No workspace; capturable in a graph. */
+gemm_status gemm_grouped_run(const gemm_grouped_plan* plan, const void* A, const void* B, const int32_t* offsets,
+                             void* D, void* stream);
+
+/* The table and the row order of a grouped product from one group id per row:
+ * order (R int32) lists the rows by ascending id, rows of one id in their own
+ * order, rows whose id is outside [0, groups) last; offsets (groups + 1 int32)
+ * holds each group's first place in it.  ids: int32 (id_bytes = 4) or int64 (8).
+ * R < 2^31, groups <= 1023.  workspace: gemm_group_rows_workspace bytes (0 for
+ * small R), 4-byte aligned, with no preparation, for one launch at a time.
+ * ids, offsets, order and workspace must not overlap. */
+gemm_status gemm_group_rows(const void* ids, int32_t id_bytes, int64_t R, int64_t groups, int32_t* offsets,
+                            int32_t* order, void* workspace, size_t workspace_bytes, void* stream);
+gemm_status gemm_group_rows_workspace(int64_t R, int64_t groups, size_t* bytes);
+
+/* ---- Matrix-vector products with 4-bit weights and group scales.
+ *
+ *     Y[m, n] = sum_k X[m, k] (q[e, n, k] - z[e, n, k / group]) s[e, n, k / group]
+ *
+ * for a few rows (a decode batch): q in 0..15, two k per byte, even k in the
+ * low nibble, k along each of the N rows; scales s of X's type and integer
+ * zero points z (one byte each; 8 without them), one per `group` (32, 64 or
+ * 128) consecutive k of a row.  e is 0, or, with experts > 0, the row's own id
+ * from a device array (one weight matrix per expert; a row whose id is outside
+ * [0, experts) gives zeros).  fp16 or bf16 X, S and Y; fp32 sums.
+ * Every finite output is within
+ *     ulp_out + 2^-20 * sum_k 31 |X[m, k] s|
+ * of the exact value (the sums run over q + 16 and are corrected: 31 bounds
+ * that offset's part).  Bitwise reproducible for a fixed plan. */
+typedef struct gemm_w4_problem {
+    int64_t M, N, K, group;     /* K a multiple of 32 */
+    int64_t experts;            /* 0: one matrix for every row; at most 65535 */
+    int64_t sx, sy;             /* row strides of X (multiple of 8) and Y, elements */
+    int64_t sw_n, sw_e;         /* W: row and expert strides, bytes, multiples of 16 */
+    int64_t ss_n, ss_e;         /* S: element strides */
+    int64_t sz_n, sz_e;         /* Z: byte strides (unused without zero points) */
+    gemm_dtype dtype;           /* GEMM_F16 or GEMM_BF16 */
+    int32_t has_zeros;
+    int32_t id_bytes;           /* 4 or 8 with experts */
+} gemm_w4_problem;
+
+typedef struct gemm_w4_plan gemm_w4_plan;   /* opaque, immutable after creation */
+
+gemm_status gemm_w4_plan_create(const gemm_w4_problem* prob, int device, gemm_w4_plan** out);
+gemm_status gemm_w4_plan_create_for(const gemm_w4_problem* prob, const gemm_device_info* info, gemm_w4_plan** out);
+void gemm_w4_plan_destroy(gemm_w4_plan* plan);
+gemm_status gemm_w4_plan_describe(const gemm_w4_plan* plan, char* buf, size_t len);
+
+/* Enqueue the product on `stream`.  X and W 16-byte aligned.  Z is NULL without
+ * has_zeros, expert_ids NULL without experts.  Y may overlap no input.  No
+ * workspace; capturable in a graph. */
+gemm_status gemm_w4_run(const gemm_w4_plan* plan, const void* X, const void* W, const void* S, const void* Z,
+                        const void* expert_ids, void* Y, void* stream);
+
 const char* gemm_status_string(gemm_status status);
 
 /* Detail of the last failure on this thread ("" if none). */
