@@ -87,6 +87,26 @@ def gemm_group_rows(ids, id_bytes, R, groups, offsets, order, workspace=None, wo
 _plans = {}
 _lock = threading.Lock()   # guards _plans
 
+# The plain calls (no out, config or stream) that passed every check, by what
+# the checks look at: the operands' types, shapes, strides and devices.  A call
+# found here goes straight to the launch: 6 us of host time instead of 11,
+# which is what the smallest products take.
+_matmul_calls, _wgrad_calls, _rows_calls = {}, {}, {}
+_MOST_CALLS = 4096
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _signature(a, b, offsets):
+    return (a.dtype, a.shape, a.stride(), a.get_device(), b.dtype, b.shape, b.stride(), b.get_device(),
+            offsets.dtype, offsets.shape, offsets.stride(), offsets.get_device())
+
+
+def _remember(calls, key, value):
+    if len(calls) >= _MOST_CALLS:   # ragged row counts: one entry each
+        calls.clear()
+    calls[key] = value
+
 
 def _need_gpu(device, *named):
     """Every tensor on `device`, a GPU."""
@@ -153,8 +173,8 @@ def _run(kind, A, B, offsets, out, groups, P, Q, accumulate, config):
             if plan is None:
                 plan = _plans[key] = gemm_grouped_plan_create(p, A.device.index, config)
     gemm_grouped_run(plan, A.data_ptr(), B.data_ptr(), offsets.data_ptr(), out.data_ptr(),
-                     torch.cuda.current_stream(A.device).cuda_stream)
-    return out
+                     _raw_stream(A.device.index))
+    return plan
 
 
 def _operands(A, B, nb):
@@ -173,6 +193,15 @@ def grouped_matmul(A, B, offsets, out=None, config=None, stream=None):
     float16 or bfloat16; offsets: E + 1 int32 on the GPU, not decreasing.
     config: optional dict of gemm_config fields to force.  Asynchronous on
     `stream` (default: torch's current stream)."""
+    key = None
+    if out is None and config is None and stream is None:
+        key = _signature(A, B, offsets)
+        hit = _matmul_calls.get(key)
+        if hit is not None and _current_device() == hit[0]:
+            dev, plan, shape = hit
+            D = A.new_empty(shape)
+            gemm_grouped_run(plan, A.data_ptr(), B.data_ptr(), offsets.data_ptr(), D.data_ptr(), _raw_stream(dev))
+            return D
     _operands(A, B, 3)
     E, K, N = B.shape
     R = A.shape[0]
@@ -185,7 +214,10 @@ def grouped_matmul(A, B, offsets, out=None, config=None, stream=None):
 
     def call():
         D = out if out is not None else torch.empty((R, N), dtype=A.dtype, device=A.device)
-        return _run(GEMM_GROUPED_ROWS, A, B, offsets, D, E, K, N, False, config)
+        plan = _run(GEMM_GROUPED_ROWS, A, B, offsets, D, E, K, N, False, config)
+        if key is not None:
+            _remember(_matmul_calls, key, (A.device.index, plan, (R, N)))
+        return D
     return _on_stream(call, A.device, stream, (A, B, offsets, out))
 
 
@@ -195,6 +227,15 @@ def grouped_wgrad(A, G, offsets, out=None, out_dtype=None, accumulate=False, con
     stored N x K is grouped_wgrad(G, A).  out_dtype: the operands' dtype (the
     default) or float32.  An empty group gives zeros.  accumulate: add to `out`
     (E x K x N) instead of overwriting it."""
+    key = None
+    if out is None and config is None and stream is None and not accumulate:
+        key = _signature(A, G, offsets) + (out_dtype,)
+        hit = _wgrad_calls.get(key)
+        if hit is not None and _current_device() == hit[0]:
+            dev, plan, shape, dtype = hit
+            D = A.new_empty(shape, dtype=dtype)
+            gemm_grouped_run(plan, A.data_ptr(), G.data_ptr(), offsets.data_ptr(), D.data_ptr(), _raw_stream(dev))
+            return D
     _operands(A, G, 2)
     if A.shape[0] != G.shape[0]:
         raise ValueError("row counts differ: %s and %s" % (tuple(A.shape), tuple(G.shape)))
@@ -213,7 +254,10 @@ def grouped_wgrad(A, G, offsets, out=None, out_dtype=None, accumulate=False, con
 
     def call():
         D = out if out is not None else torch.empty((E, K, N), dtype=dtype, device=A.device)
-        return _run(GEMM_GROUPED_REDUCE, A, G, offsets, D, E, K, N, accumulate, config)
+        plan = _run(GEMM_GROUPED_REDUCE, A, G, offsets, D, E, K, N, accumulate, config)
+        if key is not None:
+            _remember(_wgrad_calls, key, (A.device.index, plan, (E, K, N), dtype))
+        return D
     return _on_stream(call, A.device, stream, (A, G, offsets, out))
 
 
@@ -222,22 +266,34 @@ def group_rows(ids, groups, stream=None):
     order lists the rows by ascending id, rows of one id in their own order and
     rows whose id is outside [0, groups) last; offsets (groups + 1) holds each
     group's first place in it."""
+    key = None
+    if stream is None:
+        key = (ids.dtype, ids.shape, ids.stride(), ids.get_device(), groups)
+        hit = _rows_calls.get(key)
+        if hit is not None and _current_device() == hit[0]:
+            return _group_rows(ids, groups, *hit)
     if ids.dtype not in (torch.int32, torch.int64):
         raise TypeError("ids must be int32 or int64, got %s" % ids.dtype)
     if ids.dim() != 1 or (ids.shape[0] > 1 and ids.stride(0) != 1):
         raise ValueError("ids must be one contiguous dimension")
     _need_gpu(ids.device, ("ids", ids))
-    R = ids.shape[0]
 
     def call():
-        offsets = torch.empty(max(groups, 0) + 1, dtype=torch.int32, device=ids.device)
-        order = torch.empty(R, dtype=torch.int32, device=ids.device)
-        need = gemm_group_rows_workspace(R, groups)
-        ws = torch.empty(need, dtype=torch.uint8, device=ids.device) if need else None
-        gemm_group_rows(ids.data_ptr(), ids.element_size(), R, groups, offsets.data_ptr(), order.data_ptr(),
-                        ws.data_ptr() if need else None, need, torch.cuda.current_stream(ids.device).cuda_stream)
-        return offsets, order
+        hit = (ids.device.index, ids.shape[0], ids.element_size(), gemm_group_rows_workspace(ids.shape[0], groups))
+        result = _group_rows(ids, groups, *hit)
+        if key is not None:
+            _remember(_rows_calls, key, hit)
+        return result
     return _on_stream(call, ids.device, stream, (ids,))
+
+
+def _group_rows(ids, groups, device, R, id_bytes, need):
+    offsets = ids.new_empty(groups + 1, dtype=torch.int32)
+    order = ids.new_empty(R, dtype=torch.int32)
+    ws = ids.new_empty(need, dtype=torch.uint8) if need else None
+    gemm_group_rows(ids.data_ptr(), id_bytes, R, groups, offsets.data_ptr(), order.data_ptr(),
+                    ws.data_ptr() if need else None, need, _raw_stream(device))
+    return offsets, order
 
 
 class _GroupedLinear(torch.autograd.Function):
