@@ -1,7 +1,5 @@
-// The grouped products for operands that the 16-byte loads cannot take (a
-// contiguous extent or stride that is no multiple of 8 elements, an unaligned
-// base, broadcast or twice-strided views): the register-staged tile body with
-// element loads.
+// The grouped products for operands without a contiguous index (broadcast or
+// twice-strided views): the register-staged tile body with element loads.
 #include "gemm_tile_kernel.h"
 #include "grouped_kernel.h"
 
@@ -41,7 +39,7 @@ hipError_t launch_grouped_any(const GroupedArgs& a, int64_t grid, hipStream_t st
 }
 
 #define GROUPED_ANY(BM, BN, BK, WM, WN, MF, ST, BF, KIND, O32, NAME)                                          \
-    {KIND, BM, BN, BK, ST, MF, WM, WN, BF, 0, 0, O32, 64 * WM * WN, GROUPED_LDS(BM, BN, BK, ST),               \
+    {KIND, BM, BN, BK, ST, MF, WM, WN, BF, kGroupedAny, 0, O32, 64 * WM * WN, GROUPED_LDS(BM, BN, BK, ST),               \
      &launch_grouped_any<BM, BN, BK, WM, WN, MF, ST, (BF != 0), KIND, (O32 != 0)>,                            \
      NAME "<" DTG_STR(BM) "," DTG_STR(BN) "," DTG_STR(BK) "," DTG_STR(WM) "," DTG_STR(WN) "," DTG_STR(MF) "," \
      DTG_STR(ST) "," DTG_STR(BF) ">"}

@@ -206,7 +206,7 @@ hipError_t launch_grouped_reduce(const GroupedArgs& a, int64_t grid, hipStream_t
 
 #define GROUPED_LDS(BM, BN, BK, ST) static_cast<int64_t>(ST) * (BM + BN) * BK * 2
 #define GROUPED_ROWS_ENTRY(BM, BN, BK, WM, WN, MF, ST, BF, TB)                                       \
-    {kGroupedRows, BM, BN, BK, ST, MF, WM, WN, BF, 1, TB, 0, 64 * WM * WN, GROUPED_LDS(BM, BN, BK, ST), \
+    {kGroupedRows, BM, BN, BK, ST, MF, WM, WN, BF, kGroupedDirect, TB, 0, 64 * WM * WN, GROUPED_LDS(BM, BN, BK, ST), \
      &launch_grouped_rows<BM, BN, BK, WM, WN, MF, ST, (BF != 0), (TB != 0)>,                         \
      "gemm_grouped_rows_kernel<" DTG_STR(BM) "," DTG_STR(BN) "," DTG_STR(BK) "," DTG_STR(WM) ","      \
      DTG_STR(WN) "," DTG_STR(MF) "," DTG_STR(ST) "," DTG_STR(BF) "," DTG_STR(TB) ">"}
@@ -216,7 +216,7 @@ hipError_t launch_grouped_reduce(const GroupedArgs& a, int64_t grid, hipStream_t
     GROUPED_ROWS_ENTRY(BM, BN, BK, WM, WN, MF, ST, 0, 1),    \
     GROUPED_ROWS_ENTRY(BM, BN, BK, WM, WN, MF, ST, 1, 1)
 #define GROUPED_REDUCE_ENTRY(BM, BN, BK, WM, WN, MF, ST, BF, O32)                                      \
-    {kGroupedReduce, BM, BN, BK, ST, MF, WM, WN, BF, 1, 0, O32, 64 * WM * WN, GROUPED_LDS(BM, BN, BK, ST), \
+    {kGroupedReduce, BM, BN, BK, ST, MF, WM, WN, BF, kGroupedDirect, 0, O32, 64 * WM * WN, GROUPED_LDS(BM, BN, BK, ST), \
      &launch_grouped_reduce<BM, BN, BK, WM, WN, MF, ST, (BF != 0), (O32 != 0)>,                        \
      "gemm_grouped_reduce_kernel<" DTG_STR(BM) "," DTG_STR(BN) "," DTG_STR(BK) "," DTG_STR(WM) ","      \
      DTG_STR(WN) "," DTG_STR(MF) "," DTG_STR(ST) "," DTG_STR(BF) "," DTG_STR(O32) ">"}

@@ -31,13 +31,17 @@ typedef hipError_t (*grouped_launch_fn)(const GroupedArgs& args, int64_t grid, h
 
 enum GroupedKind { kGroupedRows = 0, kGroupedReduce = 1 };
 
-// One compiled variant.  tb: B[g] is stored Q x P (rows kind); vec = 1: the
-// direct-to-LDS tile (16-byte chunks), 0: the element-wise tile (any strides).
+// How a variant reads its operands: element by element (any strides), in
+// chunks of 8 of the contiguous index at any address, or straight into LDS in
+// aligned 16-byte chunks.
+enum GroupedLoads { kGroupedAny = 0, kGroupedDirect = 1, kGroupedOdd = 2 };
+
+// One compiled variant.  tb: B[g] is stored Q x P (rows kind).
 struct GroupedEntry {
     int32_t kind;
     int32_t bm, bn, bk, stages, mfma, waves_m, waves_n;
     int32_t dtype;          // 0 fp16, 1 bf16
-    int32_t vec, tb, out32;
+    int32_t loads, tb, out32;   // loads: GroupedLoads
     int32_t threads;
     int64_t lds_bytes;
     grouped_launch_fn launch;
@@ -46,6 +50,7 @@ struct GroupedEntry {
 
 const GroupedEntry* grouped_rows_table(int* count);
 const GroupedEntry* grouped_reduce_table(int* count);
+const GroupedEntry* grouped_odd_table(int* count);
 const GroupedEntry* grouped_any_table(int* count);
 
 // Row grouping: offsets (groups + 1) and the stable order of the R rows by

@@ -225,3 +225,14 @@ def test_quantize_on_the_cpu():
     assert (s == 1).all() and (z == 8).all() and q[0, 7] == 14 | 15 << 4
     q, s, z = w4.w4_quantize(torch.zeros(2, 32, dtype=torch.bfloat16), group=128)
     assert (q == 0x88).all() and torch.isfinite(s).all()
+
+
+def test_contiguous_operands_at_any_alignment_take_chunked_loads():
+    for kw in (dict(P=511), dict(sa_r=516), dict(sb_g=512 * 768 + 4), dict(sa_r=0)):
+        assert "rows_odd_any_kernel" in plan(rows_problem(**kw)).describe(), kw
+        assert "rows_odd_any_kernel" in plan(rows_problem(trans=True, **kw)).describe(), kw
+    assert "reduce_odd_any_kernel" in plan(reduce_problem(Q=763)).describe()
+    # twice-strided or shorter than a chunk: element loads
+    for kw in (dict(sa_p=2), dict(P=7), dict(Q=7)):
+        assert "rows_any_kernel" in plan(rows_problem(**kw)).describe(), kw
+    assert "reduce_any_kernel" in plan(reduce_problem(P=7)).describe()
