@@ -79,6 +79,8 @@ gemm_status validate(const gemm_w4_problem* p) {
                     (long long)p->sw_e);
     if (w_bytes(p) < 0 || s_elems(p) < 0 || z_bytes(p) < 0 || x_elems(p) < 0 || y_elems(p) < 0)
         return fail(GEMM_ERR_INVALID_ARG, "strides reach past 2^60 elements");
+    if (p->sx > kMaxDim || p->ss_n > kMaxDim || (p->has_zeros && p->sz_n > kMaxDim) || p->sw_n > kMaxDim / 32)
+        return fail(GEMM_ERR_UNSUPPORTED, "rows too far apart: X, S and Z at most 2^31-1 elements, W 2^26 bytes");
     if (p->M > 1 && p->N > 0 && p->sy < p->N)
         return fail(GEMM_ERR_INVALID_ARG, "Y row stride %lld < N=%lld makes output rows overlap", (long long)p->sy,
                     (long long)p->N);
@@ -94,16 +96,22 @@ gemm_status plan_impl(const gemm_w4_problem* prob, const gemm_device_info* dev, 
     // rows per pass: two blocks of 16 where a dense batch fills them; a
     // workgroup of an expert sees that expert's rows only
     const int mb = prob->experts == 0 && prob->M > 16 ? 2 : 1;
-    // columns per workgroup: the widest that still gives each CU one (X is
-    // read once per workgroup)
+    // Columns per workgroup, in blocks of 16.  One block, eight waves, while that
+    // gives no CU two workgroups (16 x 4096 x 4096: 8.2 us, two blocks 9.3); four
+    // blocks, eight waves, where they still reach four CUs in five (16 x 8192 x
+    // 14336: 24 us, two blocks 27; 8 x 8192 x 8192, 128 workgroups: 20 us, two
+    // blocks 15); else two blocks, four waves, two workgroups to a CU.
     int64_t used = matrices(prob);
     if (used > prob->M) used = prob->M > 0 ? prob->M : 1;
-    const int nb = mb == 1 && used * cdiv(prob->N, 32) >= dev->cu_count ? 2 : 1;
+    const int nb = used * cdiv(prob->N, 16) <= dev->cu_count                                            ? 1
+                   : mb == 1 && prob->group > 32 && 5 * used * cdiv(prob->N, 64) >= 4 * dev->cu_count ? 4
+                                                                                                        : 2;
+    const int waves = mb == 1 && nb != 2 ? 8 : 4;
     int n = 0;
     const dtg::W4Entry* t = dtg::w4_kernel_table(&n);
     const dtg::W4Entry* e = nullptr;
     for (int i = 0; i < n && !e; ++i)
-        if (t[i].nb == nb && t[i].mb == mb && t[i].group == prob->group && t[i].zeros == prob->has_zeros &&
+        if (t[i].nb == nb && t[i].waves == waves && t[i].mb == mb && t[i].group == prob->group && t[i].zeros == prob->has_zeros &&
             t[i].dtype == (prob->dtype == GEMM_BF16 ? 1 : 0))
             e = &t[i];
     if (!e) return fail(GEMM_ERR_UNSUPPORTED, "no 4-bit kernel for group %lld", (long long)prob->group);

@@ -19,14 +19,22 @@
 // output that comes out infinite or NaN (an infinity in X makes both sums
 // infinite) is summed again term by term.
 //
-// A wave takes 128 k at a time of 16 NB rows of W: each lane one 16-byte load
-// per 16 rows (row l mod 16, k 32 (l / 16) .. + 31), non-temporal, U chunks
-// ahead in registers.  The order of k inside the instruction is free as long
-// as X follows it, so with groups of 128 a lane's four dwords are simply four
+// A wave takes chunks of 128 k of 16 NB rows of W: each lane one 16-byte load
+// per 16 rows (row l mod 16, k 32 (l / 16) .. + 31), non-temporal, UW chunks
+// ahead in registers; X comes through a ring in LDS, filled by direct loads;
+// the scales and offsets of the workgroup's columns are converted into an LDS
+// table once.  The order of k inside the instruction is free as long as X
+// follows it, so with groups of 128 a lane's four dwords are simply four
 // instructions; for groups of 64 or 32 the dwords are first exchanged between
 // the wave's halves (and quarters) so that every instruction stays inside one
 // group.  The waves of a workgroup take the chunks in turn and their sums are
 // added through LDS in wave order, so a call's result does not depend on timing.
+//
+// Measured (W rotated through 350 MB, past the caches): 16 x 8192 x 14336,
+// groups of 64 with zero points, 24 us, against 13.7 us for reading W alone in
+// this order of lanes (10.5 us in consecutive 1 KB); 1 x 4096 x 4096 6.6 us.
+// Bound by issue: about 70 vector instructions per 1 KB of W, of which 32
+// unpack the nibbles, and 3 us before the first product.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -38,15 +46,22 @@ namespace {
 
 using namespace dev;
 
-constexpr int kListRows = 1024;   // rows gathered per pass over the expert ids
+constexpr int kListRows = 256;    // rows gathered per pass over the expert ids
+constexpr int kPanel = 128;       // groups of k whose scales are held in LDS at a time
+constexpr int kPitch = kPanel + 1;   // odd: 16 columns' reads of one group meet no LDS bank twice
 
-// Nibbles r and r + 4 of w as the pair (16 + q_r, 16 + q_{r + 4}).
+// Lowest mantissa bit of the units place of 16.0.
+template <bool BF16> constexpr int kUnits = BF16 ? 3 : 6;
+
+// Nibbles r and r + 4 of w as the pair (16 + q_r, 16 + q_{r + 4}); `mask` and
+// `sixteen` are the nibbles' places and two times 16.0, in registers (as
+// literals they would cost an instruction each).
 template <bool BF16, int R>
-__device__ __forceinline__ uint32_t offset_pair(uint32_t w) {
-    constexpr int to = BF16 ? 3 : 6;                    // lowest mantissa bit of the units place
+__device__ __forceinline__ uint32_t offset_pair(uint32_t w, uint32_t mask, uint32_t sixteen) {
+    constexpr int to = kUnits<BF16>;
     constexpr int sh = 4 * R - to;
     const uint32_t v = sh > 0 ? w >> (sh > 0 ? sh : 0) : w << (sh < 0 ? -sh : 0);
-    return (v & (0x000F000Fu << to)) | (BF16 ? 0x41804180u : 0x4C004C00u);
+    return (v & mask) | sixteen;
 }
 
 // X's 8 consecutive k in the nibbles' pair order: (k, k + 4) for k = 0..3.
@@ -67,23 +82,29 @@ __device__ __forceinline__ void swap_quarters(uint32_t& a, uint32_t& b) {
 }
 
 // First k (within a chunk of 128) of the 8 that lane quarter g feeds to
-// instruction t.
+// instruction t: quarter_k(g) + step_k(t).
 template <int G>
-__device__ __forceinline__ int step_k(int t, int g) {
-    if constexpr (G == 128) return 32 * g + 8 * t;
-    else if constexpr (G == 64) return 64 * (t >> 1) + 8 * (t & 1) + 32 * (g & 1) + 16 * (g >> 1);
-    else return 32 * t + 8 * g;
+__device__ __forceinline__ int quarter_k(int g) {
+    if constexpr (G == 128) return 32 * g;
+    else if constexpr (G == 64) return 32 * (g & 1) + 16 * (g >> 1);
+    else return 8 * g;
+}
+template <int G>
+constexpr int step_k(int t) {
+    return G == 128 ? 8 * t : G == 64 ? 64 * (t >> 1) + 8 * (t & 1) : 32 * t;
 }
 
 // The sum of one output by the formula, term by term in fp32: for outputs
 // that the offset form leaves infinite or NaN.
 template <int G, bool BF16, bool ZP>
-__device__ __noinline__ float plain_sum(const uint16_t* x, const uint8_t* w, const uint16_t* s, const uint8_t* z,
+__device__ __forceinline__ float plain_sum(const uint16_t* x, const uint8_t* w, const uint16_t* s, const uint8_t* z,
                                         int K) {
     float y = 0.0f;
+#pragma nounroll
     for (int k0 = 0; k0 < K; k0 += G) {
         const float zero = ZP ? static_cast<float>(z[k0 / G]) : 8.0f;
         float t = 0.0f;
+#pragma nounroll
         for (int k = k0; k < k0 + G && k < K; ++k) {
             const int q = (w[k >> 1] >> (4 * (k & 1))) & 15;
             t += widen<BF16>(x[k]) * (static_cast<float>(q) - zero);
@@ -94,11 +115,14 @@ __device__ __noinline__ float plain_sum(const uint16_t* x, const uint8_t* w, con
 }
 
 template <int NB, int MB, int NWV, int G, bool BF16, bool ZP>
-__global__ __launch_bounds__(64 * NWV) void gemm_w4_kernel(W4Args a) {
-    constexpr int NG = 128 / G;                          // groups per chunk
-    constexpr int U = NB * MB == 1 ? 4 : 2;               // chunks in flight
+__global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
+    constexpr int NG = 128 / G;          // groups per chunk
+    constexpr int UW = NB == 4 ? 2 : 4;  // chunks of W in flight, in registers
+    constexpr int UX = 2;                // chunks of X in flight, in LDS
     constexpr int ROWS = 16 * MB;
-    __shared__ float red[NWV * NB * MB * 256];
+    constexpr int CW = 16 * NB / NWV;    // columns of the table per wave
+    __shared__ float2 tab[16 * NB * kPitch];
+    __shared__ __attribute__((aligned(1024))) uint16_t xring[NWV * UX * MB * 2048];
     __shared__ int list[kListRows];
     __shared__ int listed;
 
@@ -109,24 +133,81 @@ __global__ __launch_bounds__(64 * NWV) void gemm_w4_kernel(W4Args a) {
     const int e = blockIdx.y;
     const int n0 = blockIdx.x * (16 * NB);
     const int M = a.M, N = a.N, K = a.K;
-    const uint8_t* const W = a.W + static_cast<int64_t>(e) * a.sw_e;
-    const uint16_t* const S = a.S + static_cast<int64_t>(e) * a.ss_e;
-    const uint8_t* const Z = ZP ? a.Z + static_cast<int64_t>(e) * a.sz_e : nullptr;
+    const uint8_t* const W = a.W + static_cast<int64_t>(e) * a.sw_e + static_cast<int64_t>(n0) * a.sw_n;
+    const uint16_t* const S = a.S + static_cast<int64_t>(e) * a.ss_e + static_cast<int64_t>(n0) * a.ss_n;
+    const uint8_t* const Z = ZP ? a.Z + static_cast<int64_t>(e) * a.sz_e + static_cast<int64_t>(n0) * a.sz_n : nullptr;
+    const int cols = N - n0 < 16 * NB ? N - n0 : 16 * NB;   // columns past N repeat the last one and are not stored
 
-    // this lane's columns (those past N repeat the last one and are not stored)
-    const uint8_t* wrow[NB];
-    const uint16_t* srow[NB];
-    const uint8_t* zrow[NB];
+    // this lane's bytes within the workgroup's columns (the planner keeps 64 row strides below 2^32)
+    uint32_t woff[NB];
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-        const int n = n0 + 16 * j + (lane & 15);
-        const int64_t nc = n < N ? n : N - 1;
-        wrow[j] = W + nc * a.sw_n + 16 * g;
-        srow[j] = S + nc * a.ss_n;
-        zrow[j] = ZP ? Z + nc * a.sz_n : nullptr;
+        const int n = 16 * j + (lane & 15);
+        woff[j] = static_cast<uint32_t>(n < cols ? n : cols - 1) * static_cast<uint32_t>(a.sw_n) + 16 * g;
     }
     const int full = K / 128;
+    const int groups = (K + G - 1) / G;
 
+    // {scale, offset} of groups [p0, p0 + held) of every column, zeros up to a multiple of 4.
+    // In two steps, all loads before the first store: loaded and stored one by
+    // one, the table took half of a wave's time.  Half a wave per column, four
+    // groups per lane.
+    struct __attribute__((packed, aligned(2))) Loose8 {
+        uint32_t v[2];
+    };
+    struct __attribute__((packed, aligned(1))) Loose4 {
+        uint32_t v;
+    };
+    const int tcol = wave * CW + (lane >> 5), tgroup = 4 * (lane & 31);   // columns tcol + 2 c, groups tgroup + 0..3
+    uint32_t ts[CW / 2][2], tz[CW / 2];
+    auto load_table = [&](int p0, int held) {
+#pragma unroll
+        for (int c = 0; c < CW / 2; ++c) {
+            const uint32_t n = tcol + 2 * c < cols ? tcol + 2 * c : cols - 1;
+            const uint16_t* s = S + static_cast<uint64_t>(n) * static_cast<uint32_t>(a.ss_n) + p0;
+            const uint8_t* z = ZP ? Z + static_cast<uint64_t>(n) * static_cast<uint32_t>(a.sz_n) + p0 : nullptr;
+            ts[c][0] = ts[c][1] = 0;
+            tz[c] = 0x08080808u;
+            if (held % 4 == 0) {
+                if (tgroup < held) {
+                    const Loose8 v = *reinterpret_cast<const Loose8*>(s + tgroup);
+                    ts[c][0] = v.v[0];
+                    ts[c][1] = v.v[1];
+                    if constexpr (ZP) tz[c] = reinterpret_cast<const Loose4*>(z + tgroup)->v;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (tgroup + i < held) {
+                        ts[c][i / 2] |= static_cast<uint32_t>(s[tgroup + i]) << (16 * (i % 2));
+                        if constexpr (ZP) tz[c] = (tz[c] & ~(255u << (8 * i))) | static_cast<uint32_t>(z[tgroup + i]) << (8 * i);
+                    }
+            }
+        }
+    };
+    auto store_table = [&](int held) {
+#pragma unroll
+        for (int c = 0; c < CW / 2; ++c) {
+            float2* row = tab + (tcol + 2 * c) * kPitch;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (tgroup < held)
+                    row[tgroup + i] = float2{widen<BF16>(static_cast<uint16_t>(ts[c][i / 2] >> (16 * (i % 2)))),
+                                             16.0f + static_cast<float>((tz[c] >> (8 * i)) & 255u)};
+        }
+    };
+    int in_table = -1;   // first group of the table's panel
+    float* const red = reinterpret_cast<float*>(xring);
+    uint16_t* const xwave = xring + wave * UX * MB * 2048;
+    uint32_t xaddr[4];   // this lane's pieces of X: instruction row lane % 16
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+        xaddr[t] = lds_addr(xwave) + (lane & 15) * 256 +
+                   (((quarter_k<G>(g) + step_k<G>(t)) / 8) ^ (lane & 15)) * 16;
+    const uint32_t tab_addr = lds_addr(reinterpret_cast<const uint16_t*>(tab)) + (lane & 15) * (kPitch * 8);
+
+    uint32_t mask = 0x000F000Fu << kUnits<BF16>, sixteen = BF16 ? 0x41804180u : 0x4C004C00u;
+    asm volatile("" : "+s"(mask), "+v"(sixteen));
     u32x4 ones;
 #pragma unroll
     for (int r = 0; r < 4; ++r) ones[r] = BF16 ? 0x3F803F80u : 0x3C003C00u;
@@ -151,25 +232,57 @@ __global__ __launch_bounds__(64 * NWV) void gemm_w4_kernel(W4Args a) {
                     n += __popcll(hits);
                     // rows of no expert are zeros, written by the first expert's workgroups
                     if (e == 0 && row < end && (id < 0 || id >= a.num_experts))
-                        for (int c = n0; c < n0 + 16 * NB && c < N; ++c)
-                            a.Y[static_cast<int64_t>(row) * a.sy + c] = 0;
+                        for (int c = 0; c < cols; ++c) a.Y[static_cast<int64_t>(row) * a.sy + n0 + c] = 0;
                 }
                 if (lane == 0) listed = n;
             }
             __syncthreads();
-            rows = listed;
+            rows = __builtin_amdgcn_readfirstlane(listed);
         } else {
             rows = M - first < kListRows ? M - first : kListRows;
         }
         auto row_of = [&](int i) { return a.experts ? list[i] : first + i; };
 
         for (int m0 = 0; m0 < rows; m0 += ROWS) {
-            const uint16_t* xrow[MB];
+            u32x4 w[UW][NB];
+            auto load_w = [&](u32x4 (&d)[NB], int chunk) {
+                const uint8_t* wk = W + static_cast<int64_t>(chunk) * 64;
 #pragma unroll
-            for (int b = 0; b < MB; ++b) {
-                const int i = m0 + 16 * b + (lane & 15);
-                xrow[b] = a.X + static_cast<int64_t>(row_of(i < rows ? i : rows - 1)) * a.sx;
-            }
+                for (int j = 0; j < NB; ++j)
+                    d[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wk + woff[j]));
+            };
+            // The wave's whole chunks of the panel from group p0 on: c0 + wave,
+            // c0 + wave + NWV, ... (`mine` of them); W of the first ones is on its
+            // way before anything else is computed.
+            int c0, mine;
+            auto at = [&](int i) { return wave + (i < mine ? i : mine - 1) * NWV; };
+            auto start = [&](int p0) {
+                c0 = p0 / NG;
+                mine = ((full < c0 + kPanel / NG ? full : c0 + kPanel / NG) - c0 - wave + NWV - 1) / NWV;
+                if (mine > 0)
+#pragma unroll
+                    for (int u = 0; u < UW - 1; ++u) load_w(w[u], c0 + at(u));
+            };
+            start(0);
+            // Row i of a block of 16 sits in instruction row 4 (i % 4) + i / 4, so
+            // that register r of the result holds rows 4 r .. 4 r + 3: blocks of up
+            // to 4 rows scale one register in place of four.
+            // X goes to LDS a chunk at a time, each wave its own: load t brings
+            // instruction rows 4 t .. 4 t + 3, 256 bytes of each in one piece (read
+            // straight into the operand's lanes, consecutive lanes lie in different
+            // rows, and the 16-row product took 32 us in place of 27).  Piece p of
+            // row r sits at p ^ r.
+            const uint16_t* xsrc[MB][4];
+#pragma unroll
+            for (int b = 0; b < MB; ++b)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const int ir = 4 * t + g, i = m0 + 16 * b + t + 4 * g;
+                    xsrc[b][t] = a.X + static_cast<uint64_t>(static_cast<uint32_t>(row_of(i < rows ? i : rows - 1))) *
+                                           static_cast<uint32_t>(a.sx) +
+                                 8 * ((lane & 15) ^ ir);
+                }
+            const bool few = rows - m0 <= 4;
 
             f32x4 tot[MB][NB];
 #pragma unroll
@@ -177,42 +290,60 @@ __global__ __launch_bounds__(64 * NWV) void gemm_w4_kernel(W4Args a) {
 #pragma unroll
                 for (int j = 0; j < NB; ++j) tot[b][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-            struct Chunk {
-                u32x4 w[NB];
-                u32x4 x[MB][4];
-                uint16_t s[NB][NG];
-                uint8_t z[NB][NG];
-            };
-            auto load = [&](Chunk& c, int chunk) {
-                const int k0 = chunk * 128;
-#pragma unroll
-                for (int j = 0; j < NB; ++j)
-                    c.w[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wrow[j] + k0 / 2));
+            auto load_x = [&](int slot, int chunk) {
 #pragma unroll
                 for (int b = 0; b < MB; ++b)
 #pragma unroll
                     for (int t = 0; t < 4; ++t)
-                        c.x[b][t] = *reinterpret_cast<const u32x4*>(xrow[b] + k0 + step_k<G>(t, g));
-#pragma unroll
-                for (int j = 0; j < NB; ++j)
-#pragma unroll
-                    for (int i = 0; i < NG; ++i) {
-                        c.s[j][i] = srow[j][chunk * NG + i];
-                        if constexpr (ZP) c.z[j][i] = zrow[j][chunk * NG + i];
-                    }
+                        __builtin_amdgcn_global_load_lds(
+                            (const __attribute__((address_space(1))) void*)(xsrc[b][t] + static_cast<int64_t>(chunk) * 128),
+                            (lds_void_t*)(xwave + (slot * MB + b) * 2048 + t * 512), 16, 0, 0);
             };
-            auto contract = [&](Chunk& c) {
+            // A chunk's operands out of LDS: X of `slot`, its groups from number `g0`
+            // of the table on.  The reads are explicit: the compiler would hold each
+            // until every load in flight to LDS has landed.
+            struct Frag {
+                u32x4 x[MB][4];
+                u32x2 q[NG][NB];
+            };
+            auto fetch = [&](auto slot_tag, Frag& f, int g0) {
+                static_for<4>([&](auto t_tag) {
+                    static_for<MB>([&](auto b_tag) {
+                        constexpr int T = decltype(t_tag)::value, B = decltype(b_tag)::value;
+                        f.x[B][T] = lds_read16<(decltype(slot_tag)::value * MB + B) * 4096>(xaddr[T]);
+                    });
+                });
+                const uint32_t taddr = tab_addr + 8 * g0;
+                static_for<NG>([&](auto i_tag) {
+                    static_for<NB>([&](auto j_tag) {
+                        constexpr int I = decltype(i_tag)::value, J = decltype(j_tag)::value;
+                        f.q[I][J] = lds_read8<(16 * J * kPitch + I) * 8>(taddr);
+                    });
+                });
+            };
+            auto landed = [&](Frag& f) {
+                lds_wait_all();
+#pragma unroll
+                for (int b = 0; b < MB; ++b)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) tie(f.x[b][t]);
+#pragma unroll
+                for (int i = 0; i < NG; ++i)
+#pragma unroll
+                    for (int j = 0; j < NB; ++j) tie(f.q[i][j]);
+            };
+            auto contract = [&](const Frag& f, u32x4 (&w)[NB]) {
                 if constexpr (G < 128) {
 #pragma unroll
                     for (int j = 0; j < NB; ++j) {
-                        uint32_t d0 = c.w[j][0], d1 = c.w[j][1], d2 = c.w[j][2], d3 = c.w[j][3];
+                        uint32_t d0 = w[j][0], d1 = w[j][1], d2 = w[j][2], d3 = w[j][3];
                         swap_halves(d0, d2);
                         swap_halves(d1, d3);
                         if constexpr (G == 32) {
                             swap_quarters(d0, d1);
                             swap_quarters(d2, d3);
                         }
-                        c.w[j] = u32x4{d0, d1, d2, d3};
+                        w[j] = u32x4{d0, d1, d2, d3};
                     }
                 }
                 f32x4 acc[MB][NB], sum[MB];
@@ -230,100 +361,130 @@ __global__ __launch_bounds__(64 * NWV) void gemm_w4_kernel(W4Args a) {
                     u32x4 wf[NB];
 #pragma unroll
                     for (int j = 0; j < NB; ++j) {
-                        const uint32_t w = c.w[j][T];
-                        wf[j] = u32x4{offset_pair<BF16, 0>(w), offset_pair<BF16, 1>(w), offset_pair<BF16, 2>(w),
-                                      offset_pair<BF16, 3>(w)};
+                        const uint32_t d = w[j][T];
+                        wf[j] = u32x4{offset_pair<BF16, 0>(d, mask, sixteen), offset_pair<BF16, 1>(d, mask, sixteen),
+                                      offset_pair<BF16, 2>(d, mask, sixteen), offset_pair<BF16, 3>(d, mask, sixteen)};
                     }
 #pragma unroll
                     for (int b = 0; b < MB; ++b) {
-                        const u32x4 xf = pair_order(c.x[b][T]);
+                        const u32x4 xf = pair_order(f.x[b][T]);
                         sum[b] = mfma<16, BF16>(xf, ones, sum[b]);
 #pragma unroll
                         for (int j = 0; j < NB; ++j) acc[b][j] = mfma<16, BF16>(xf, wf[j], acc[b][j]);
                     }
                     if constexpr (T % STEPS == STEPS - 1) {
                         constexpr int I = T / STEPS;
-#pragma unroll
-                        for (int j = 0; j < NB; ++j) {
-                            const float sc = widen<BF16>(c.s[j][I]);
-                            const float off = ZP ? 16.0f + static_cast<float>(c.z[j][I]) : 24.0f;
+                        auto scale = [&](int r) {
 #pragma unroll
                             for (int b = 0; b < MB; ++b)
 #pragma unroll
-                                for (int r = 0; r < 4; ++r)
-                                    tot[b][j][r] += sc * (acc[b][j][r] - off * sum[b][r]);
+                                for (int j = 0; j < NB; ++j)
+                                    tot[b][j][r] += __uint_as_float(f.q[I][j][0]) *
+                                                    (acc[b][j][r] - __uint_as_float(f.q[I][j][1]) * sum[b][r]);
+                        };
+                        scale(0);
+                        if (!few) {
+                            scale(1);
+                            scale(2);
+                            scale(3);
                         }
                     }
                 });
             };
 
-            // whole chunks wave, wave + NWV, ...
-            const int mine = full > wave ? (full - wave + NWV - 1) / NWV : 0;
-            if (mine > 0) {
-                Chunk c[U];
-                auto at = [&](int i) { return wave + (i < mine ? i : mine - 1) * NWV; };
-#pragma unroll
-                for (int u = 0; u < U; ++u) load(c[u], at(u));
-                for (int i = 0; i < mine; i += U) {
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        if (i + u < mine) {
-                            contract(c[u]);
-                            load(c[u], at(i + u + U));
+            for (int p0 = 0; p0 < groups; p0 += kPanel) {
+                const int held = groups - p0 < kPanel ? groups - p0 : kPanel;
+                if (mine > 0) {
+                    load_x(0, c0 + at(0));
+                    load_x(1, c0 + at(1));
+                }
+                if (in_table != p0) {
+                    load_table(p0, held);
+                    if (in_table >= 0) __syncthreads();   // the last panel's readers are done
+                    store_table(held);
+                    in_table = p0;
+                    __syncthreads();
+                }
+                // Step i contracts chunk i while the next one's operands come out of
+                // LDS, then refills their slot of the ring and W's registers.  X goes
+                // out before W: waiting for the next X leaves a later step of X and two
+                // of W in flight.
+                Frag f[2];
+                auto step = [&](auto u_tag, int i) {
+                    constexpr int V = decltype(u_tag)::value, S1 = (V + 1) % UX;
+                    wait_vm<2 * NB + 4 * MB>();
+                    fetch(std::integral_constant<int, S1>{}, f[S1], at(i + 1) * NG);
+                    contract(f[V % UX], w[V]);
+                    landed(f[S1]);
+                    load_x(S1, c0 + at(i + 3));
+                    load_w(w[V], c0 + at(i + UW));
+                };
+                if (mine > 0) {
+                    wait_vm<4 * MB>();
+                    fetch(std::integral_constant<int, 0>{}, f[0], at(0) * NG);
+                    landed(f[0]);
+                    load_x(0, c0 + at(2));
+                    load_w(w[UW - 1], c0 + at(UW - 1));
+                    for (int i = 0;; i += UW) {
+                        step(std::integral_constant<int, 0>{}, i);
+                        if (i + 1 >= mine) break;
+                        step(std::integral_constant<int, 1>{}, i + 1);
+                        if (i + 2 >= mine) break;
+                        if constexpr (UW == 4) {
+                            step(std::integral_constant<int, 2>{}, i + 2);
+                            if (i + 3 >= mine) break;
+                            step(std::integral_constant<int, 3>{}, i + 3);
+                            if (i + 4 >= mine) break;
                         }
                     }
+                    wait_vm<0>();   // no load may still be writing the ring
                 }
-            }
-            // the last K mod 128: one wave, lanes past K read the chunk's start and X as zeros
-            if (K % 128 != 0 && wave == full % NWV) {
-                Chunk c;
-                const int k0 = full * 128;
-                const bool in = k0 + 32 * g < K;
+                // the last K mod 128: one wave, lanes past K read the chunk's start and X as zeros
+                if (K % 128 != 0 && p0 + kPanel >= groups && wave == full % NWV) {
+                    const int k0 = full * 128;
+                    const uint8_t* wk = W + static_cast<int64_t>(full) * 64;
+                    const uint32_t back = k0 + 32 * g < K ? 0 : 16 * g;
 #pragma unroll
-                for (int j = 0; j < NB; ++j)
-                    c.w[j] = *reinterpret_cast<const u32x4*>(wrow[j] + k0 / 2 - (in ? 0 : 16 * g));
+                    for (int j = 0; j < NB; ++j) w[0][j] = *reinterpret_cast<const u32x4*>(wk + (woff[j] - back));
 #pragma unroll
-                for (int b = 0; b < MB; ++b)
+                    for (int b = 0; b < MB; ++b)
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const int k = k0 + step_k<G>(t, g);
-                        c.x[b][t] = u32x4{0, 0, 0, 0};
-                        if (k < K) c.x[b][t] = *reinterpret_cast<const u32x4*>(xrow[b] + k);
-                    }
-#pragma unroll
-                for (int j = 0; j < NB; ++j)
-#pragma unroll
-                    for (int i = 0; i < NG; ++i) {
-                        const bool has = k0 + i * G < K;
-                        c.s[j][i] = has ? srow[j][full * NG + i] : static_cast<uint16_t>(0);
-                        if constexpr (ZP) c.z[j][i] = has ? zrow[j][full * NG + i] : static_cast<uint8_t>(0);
-                    }
-                contract(c);
+                        for (int t = 0; t < 4; ++t) {
+                            u32x4 v = {0, 0, 0, 0};
+                            if (k0 + 8 * ((lane & 15) ^ (4 * t + g)) < K)
+                                v = *reinterpret_cast<const u32x4*>(xsrc[b][t] + k0);
+                            *reinterpret_cast<u32x4*>(xwave + b * 2048 + t * 512 + 8 * lane) = v;
+                        }
+                    lds_wait_all();
+                    fetch(std::integral_constant<int, 0>{}, f[0], (full - c0) * NG);
+                    landed(f[0]);
+                    contract(f[0], w[0]);
+                }
+                if (p0 + kPanel < groups) start(p0 + kPanel);
             }
 
-            // ---- the waves' sums in wave order, rounded once
+            // ---- the waves' sums in wave order, rounded once (over the ring)
+            __syncthreads();
 #pragma unroll
             for (int b = 0; b < MB; ++b)
 #pragma unroll
                 for (int j = 0; j < NB; ++j)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        red[(wave * MB * NB + b * NB + j) * 256 + (4 * g + r) * 16 + (lane & 15)] = tot[b][j][r];
+                        red[(wave * MB * NB + b * NB + j) * 256 + (g + 4 * r) * 16 + (lane & 15)] = tot[b][j][r];
             __syncthreads();
             for (int x = tid; x < NB * MB * 256; x += 64 * NWV) {
                 const int col = x % 16, row = (x / 16) % 16, blk = x / 256;
-                const int i = m0 + 16 * (blk / NB) + row, n = n0 + 16 * (blk % NB) + col;
-                if (i >= rows || n >= N) continue;
+                const int i = m0 + 16 * (blk / NB) + row, n = 16 * (blk % NB) + col;
+                if (i >= rows || n >= cols) continue;
                 float v = 0.0f;
 #pragma unroll
                 for (int w = 0; w < NWV; ++w) v += red[(w * MB * NB + blk) * 256 + row * 16 + col];
-                const int r = row_of(i);
+                const int64_t r = row_of(i);
                 if (!__builtin_isfinite(v))
-                    v = plain_sum<G, BF16, ZP>(a.X + static_cast<int64_t>(r) * a.sx,
-                                               W + static_cast<int64_t>(n) * a.sw_n,
-                                               S + static_cast<int64_t>(n) * a.ss_n,
-                                               ZP ? Z + static_cast<int64_t>(n) * a.sz_n : nullptr, K);
-                a.Y[static_cast<int64_t>(r) * a.sy + n] = narrow<BF16>(v);
+                    v = plain_sum<G, BF16, ZP>(a.X + r * a.sx, W + n * a.sw_n, S + n * a.ss_n,
+                                               ZP ? Z + n * a.sz_n : nullptr, K);
+                a.Y[r * a.sy + n0 + n] = narrow<BF16>(v);
             }
             __syncthreads();   // red is written again by the next block of rows
         }
@@ -343,15 +504,17 @@ hipError_t launch_w4(const W4Args& a, int64_t tiles, hipStream_t stream) {
 #define W4_ENTRY(NB, MB, NWV, G, BF, ZP)                                                     \
     {NB, MB, NWV, G, BF, ZP, &launch_w4<NB, MB, NWV, G, (BF != 0), (ZP != 0)>,               \
      "gemm_w4_kernel<" DTG_STR(NB) "," DTG_STR(MB) "," DTG_STR(NWV) "," DTG_STR(G) "," DTG_STR(BF) "," DTG_STR(ZP) ">"}
-#define W4_GROUPS(NB, MB, NWV)                                                                                   \
+// (groups of 32 keep twice the scales in registers: four column blocks would spill)
+#define W4_WIDE(NB, MB, NWV)                                                                                     \
     W4_ENTRY(NB, MB, NWV, 128, 0, 0), W4_ENTRY(NB, MB, NWV, 128, 0, 1), W4_ENTRY(NB, MB, NWV, 128, 1, 0),         \
     W4_ENTRY(NB, MB, NWV, 128, 1, 1), W4_ENTRY(NB, MB, NWV, 64, 0, 0), W4_ENTRY(NB, MB, NWV, 64, 0, 1),           \
-    W4_ENTRY(NB, MB, NWV, 64, 1, 0), W4_ENTRY(NB, MB, NWV, 64, 1, 1), W4_ENTRY(NB, MB, NWV, 32, 0, 0),            \
-    W4_ENTRY(NB, MB, NWV, 32, 0, 1), W4_ENTRY(NB, MB, NWV, 32, 1, 0), W4_ENTRY(NB, MB, NWV, 32, 1, 1)
+    W4_ENTRY(NB, MB, NWV, 64, 1, 0), W4_ENTRY(NB, MB, NWV, 64, 1, 1)
+#define W4_GROUPS(NB, MB, NWV)                                                                                   \
+    W4_WIDE(NB, MB, NWV), W4_ENTRY(NB, MB, NWV, 32, 0, 0), W4_ENTRY(NB, MB, NWV, 32, 0, 1),                       \
+    W4_ENTRY(NB, MB, NWV, 32, 1, 0), W4_ENTRY(NB, MB, NWV, 32, 1, 1)
 
 const W4Entry kTable[] = {
-    W4_GROUPS(1, 1, 8), W4_GROUPS(2, 1, 8),
-    W4_GROUPS(1, 2, 8),
+    W4_GROUPS(1, 1, 8), W4_GROUPS(2, 1, 4), W4_WIDE(4, 1, 8), W4_GROUPS(1, 2, 4), W4_GROUPS(2, 2, 4),
 };
 
 }  // namespace

@@ -376,10 +376,10 @@ gemm_status gemm_group_rows_workspace(int64_t R, int64_t groups, size_t* bytes);
 typedef struct gemm_w4_problem {
     int64_t M, N, K, group;     /* K a multiple of 32 */
     int64_t experts;            /* 0: one matrix for every row; at most 65535 */
-    int64_t sx, sy;             /* row strides of X (multiple of 8) and Y, elements */
-    int64_t sw_n, sw_e;         /* W: row and expert strides, bytes, multiples of 16 */
-    int64_t ss_n, ss_e;         /* S: element strides */
-    int64_t sz_n, sz_e;         /* Z: byte strides (unused without zero points) */
+    int64_t sx, sy;             /* row strides of X (multiple of 8, below 2^31) and Y, elements */
+    int64_t sw_n, sw_e;         /* W: row (below 2^26) and expert strides, bytes, multiples of 16 */
+    int64_t ss_n, ss_e;         /* S: element strides, ss_n below 2^31 */
+    int64_t sz_n, sz_e;         /* Z: byte strides, sz_n below 2^31 (unused without zero points) */
     gemm_dtype dtype;           /* GEMM_F16 or GEMM_BF16 */
     int32_t has_zeros;
     int32_t id_bytes;           /* 4 or 8 with experts */
