@@ -119,6 +119,8 @@ SIGNATURES = [
      [_p, ctypes.POINTER(_i64), ctypes.POINTER(_i32), ctypes.POINTER(_i64)]),
     ("gemm_grouped_plan_describe", ctypes.c_int, [_p, ctypes.c_char_p, ctypes.c_size_t]),
     ("gemm_grouped_run", ctypes.c_int, [_p, _p, _p, _p, _p, _p]),
+    ("gemm_grouped_workspace", ctypes.c_int, [_p, ctypes.POINTER(ctypes.c_size_t)]),
+    ("gemm_grouped_run_parts", ctypes.c_int, [_p, _p, _p, _p, _p, _p, ctypes.c_size_t, _p]),
     ("gemm_group_rows", ctypes.c_int, [_p, _i32, _i64, _i64, _p, _p, _p, ctypes.c_size_t, _p]),
     ("gemm_group_rows_workspace", ctypes.c_int, [_i64, _i64, ctypes.POINTER(ctypes.c_size_t)]),
     ("gemm_w4_plan_create", ctypes.c_int, [ctypes.POINTER(gemm_w4_problem), ctypes.c_int, ctypes.POINTER(_p)]),

@@ -20,6 +20,10 @@ struct gemm_grouped_plan {
     const dtg::GroupedEntry* entry;
     const dtg::GroupedEntry* fallback;   // for bases that are not 16-byte aligned
     int64_t grid;
+    // with a workspace: groups cut into parts of part_rows (0: never)
+    const dtg::GroupedEntry* part_entry;
+    int32_t part_rows;
+    int64_t max_parts;
 };
 
 namespace {
@@ -36,6 +40,9 @@ gemm_status fail(gemm_status st, const char* fmt, ...) {
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxGroups = 65535;
+constexpr double kMostPartBytes = 256e6;   // of workspace for a gradient's parts
+// mean rows of a group from which the weight gradient takes the longest first
+constexpr int64_t kSortRows = 256;
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Elements from the first to one past the last of a strided box (0 when it is
@@ -149,36 +156,101 @@ const dtg::GroupedEntry* find_entry(const gemm_grouped_problem* p, const gemm_de
     return nullptr;
 }
 
-// Tile by estimated time: rounds of workgroups, ceil(tiles / (CUs x resident
-// workgroups)), times the tile's cost per round (the dense planner's measured
-// costs).  The host knows only the mean group length: a group of r rows counts
-// r / bm tiles and half a tile for its ragged end, at least one.
-void choose_tile(const gemm_grouped_problem* p, const gemm_device_info& dev, gemm_config* want) {
-    struct T { int bm, bn, st, resident; double cost; };
-    static const T ladder[] = {{256, 256, 2, 1, 1.0}, {128, 256, 3, 1, 0.64}, {128, 128, 4, 1, 0.43},
-                               {128, 128, 2, 2, 0.68}, {64, 64, 4, 2, 0.27}};
-    double best = 0.0;
+// What a compiled tile costs, measured on gfx950: microseconds per 64 k of one
+// workgroup with the card to itself and with `resident` on every CU, and the
+// part of its output's time that other workgroups do not hide.
+struct TileCost {
+    int bm, bn, bk, st, resident;
+    double alone, loaded, shown;
+};
+constexpr TileCost kRowTiles[] = {{256, 256, 64, 2, 1, 1.2, 1.6, 1.0}, {128, 256, 64, 3, 1, 0.69, 1.05, 1.0},
+                                  {128, 128, 64, 4, 1, 0.6, 0.7, 1.0}, {128, 128, 64, 2, 2, 0.74, 1.1, 0.5},
+                                  {64, 64, 64, 4, 2, 0.3, 0.5, 0.5}};
+constexpr TileCost kReduceTiles[] = {{256, 256, 64, 2, 1, 1.2, 1.6, 1.0}, {128, 256, 64, 3, 1, 0.69, 1.05, 1.0},
+                                     {128, 128, 64, 2, 2, 0.74, 1.1, 0.5}, {128, 128, 32, 2, 4, 1.05, 2.2, 0.25},
+                                     {64, 64, 64, 4, 2, 0.3, 0.5, 0.5}};
+constexpr double kStart = 4.0;          // us before a workgroup's first product and after its last
+constexpr double kBytesPerUs = 4.7e6;   // what large copies reach
+
+gemm_config tile_config(const TileCost& t) {
+    gemm_config c;
+    memset(&c, 0, sizeof c);
+    c.bm = t.bm;
+    c.bn = t.bn;
+    c.bk = t.bk;
+    c.stages = t.st;
+    return c;
+}
+
+// Time of `items` workgroups of `steps` 64-k steps each, the longest of
+// `longest` steps.
+double workgroups_us(const TileCost& t, double items, double steps, double longest, int cus) {
+    const double slots = static_cast<double>(cus) * t.resident;
+    if (items <= cus) return kStart + longest * t.alone;
+    const double one = kStart + longest * t.loaded;
+    const double all = items / slots * (kStart + steps * t.loaded);
+    return all > one ? all : one;
+}
+
+// Rows kind: the host knows only the mean group length; a group of r rows
+// counts r / bm tiles and half a tile for its ragged end, at least one.  B is
+// read once from memory, whatever the tile.
+void choose_rows_tile(const gemm_grouped_problem* p, const gemm_device_info& dev, gemm_config* want) {
     const double groups = static_cast<double>(p->groups < p->R ? p->groups : p->R);
-    for (const T& t : ladder) {
-        gemm_config c;
-        memset(&c, 0, sizeof c);
-        c.bm = t.bm;
-        c.bn = t.bn;
-        c.stages = t.st;
+    const double steps = static_cast<double>(cdiv(p->P, 64));
+    const double bytes = 2.0 * (static_cast<double>(p->R) * p->P + groups * p->P * p->Q + static_cast<double>(p->R) * p->Q);
+    double best = 0.0;
+    for (const TileCost& t : kRowTiles) {
+        const gemm_config c = tile_config(t);
         if (!find_entry(p, dev, dtg::kGroupedDirect, c)) continue;
-        double tiles;
-        if (reduce_kind(p)) {
-            tiles = static_cast<double>(p->groups * cdiv(p->P, t.bm) * cdiv(p->Q, t.bn));
-        } else {
-            const double per = static_cast<double>(p->R) / (groups > 0 ? groups : 1) / t.bm + 0.5;
-            tiles = (groups > 0 ? groups : 1) * (per > 1 ? per : 1) * cdiv(p->Q, t.bn);
-        }
-        const double slots = static_cast<double>(dev.cu_count) * t.resident;
-        const double rounds = static_cast<double>(static_cast<int64_t>((tiles + slots - 1) / slots));
-        const double est = (rounds > 1 ? rounds : 1) * t.cost;
+        const double per = groups > 0 ? static_cast<double>(p->R) / groups / t.bm + 0.5 : 1.0;
+        const double items = (groups > 0 ? groups : 1) * (per > 1 ? per : 1) * cdiv(p->Q, t.bn);
+        double est = workgroups_us(t, items, steps, steps, dev.cu_count);
+        // the last round of many is half empty on average
+        if (items > dev.cu_count * t.resident) est += 0.5 * (kStart + steps * t.loaded);
+        const double memory = bytes / kBytesPerUs;
+        est = (est > memory ? est : memory) + 0.1 * est;
         if (best == 0.0 || est < best) {
             best = est;
             *want = c;
+        }
+    }
+}
+
+// Reduce kind: the tile, and whether to cut the groups' rows into parts (few
+// output tiles, many rows: 12000 rows of one 264 x 520 gradient 58 us whole,
+// 25 us in parts of 704).  Lengths vary: the longest group counts 1.5 means.
+void choose_reduce_tile(const gemm_grouped_problem* p, const gemm_device_info& dev, gemm_config* want,
+                        int32_t* part_rows) {
+    const double groups = static_cast<double>(p->groups > 0 ? p->groups : 1);
+    const double rows = static_cast<double>(p->R) / groups;
+    const double longest = groups > 1 && 1.5 * rows < p->R ? 1.5 * rows : static_cast<double>(p->R);
+    const double sums = static_cast<double>(p->P) * p->Q * 4;
+    const double out = groups * sums / (p->out == GEMM_GROUPED_OUT_F32 ? 1 : 2) / kBytesPerUs;
+    auto steps = [](double r) { return r > 64 ? r / 64 : 1.0; };
+    double best = 0.0;
+    for (const TileCost& t : kReduceTiles) {
+        const gemm_config c = tile_config(t);
+        if (!find_entry(p, dev, dtg::kGroupedDirect, c)) continue;
+        const double tiles = static_cast<double>(cdiv(p->P, t.bm) * cdiv(p->Q, t.bn));
+        const double work = workgroups_us(t, groups * tiles, steps(rows), steps(longest), dev.cu_count);
+        const double est = work > out ? work + t.shown * out : out + t.shown * work;
+        if (best == 0.0 || est < best) {
+            best = est;
+            *want = c;
+            *part_rows = 0;
+        }
+        for (int32_t q : {512, 768, 1024, 1536, 2048, 4096}) {
+            const double parts = static_cast<double>(p->R / q + p->groups);
+            if (p->groups == 0 || q >= longest || parts * sums > kMostPartBytes) continue;
+            // their sums are written, read again, and a second launch adds them
+            const double cut = workgroups_us(t, parts * tiles, q / 64, q / 64, dev.cu_count) +
+                               2 * parts * sums / kBytesPerUs + out + 8.0;
+            if (cut < best) {
+                best = cut;
+                *want = c;
+                *part_rows = q;
+            }
         }
     }
 }
@@ -209,7 +281,11 @@ gemm_status plan_impl(const gemm_grouped_problem* prob, const gemm_device_info* 
     // chunked loads where an index is contiguous (777 x 1003 x 517 over 5 groups: 10.8 us, 200 us element by element)
     const dtg::GroupedLoads loose = odd_ok(prob) ? dtg::kGroupedOdd : dtg::kGroupedAny;
     const dtg::GroupedLoads loads = vec_ok(prob) ? dtg::kGroupedDirect : loose;
-    if (loads == dtg::kGroupedDirect && !forced) choose_tile(prob, *dev, &want);
+    int32_t part_rows = 0;
+    if (loads == dtg::kGroupedDirect && !forced) {
+        if (reduce_kind(prob)) choose_reduce_tile(prob, *dev, &want, &part_rows);
+        else choose_rows_tile(prob, *dev, &want);
+    }
     const dtg::GroupedEntry* e = find_entry(prob, *dev, loads, want);
     const dtg::GroupedEntry* any = find_entry(prob, *dev, loose, none);
     if (!e || !any)
@@ -225,6 +301,18 @@ gemm_status plan_impl(const gemm_grouped_problem* prob, const gemm_device_info* 
     pl->entry = e;
     pl->fallback = any;
     pl->grid = grid_of(prob, e);
+    pl->part_entry = nullptr;
+    pl->part_rows = 0;
+    pl->max_parts = 0;
+    if (part_rows > 0) {
+        gemm_grouped_problem sums = *prob;
+        sums.out = GEMM_GROUPED_OUT_F32;
+        pl->part_entry = find_entry(&sums, *dev, loads, want);
+        if (pl->part_entry) {
+            pl->part_rows = part_rows;
+            pl->max_parts = prob->R / part_rows + prob->groups;
+        }
+    }
     gemm_config& c = pl->cfg;
     c = none;
     c.bm = e->bm;
@@ -290,14 +378,26 @@ gemm_status gemm_grouped_plan_describe(const gemm_grouped_plan* plan, char* buf,
     const gemm_config& c = plan->cfg;
     snprintf(buf, len,
              "kernel=%s bm=%d bn=%d bk=%d stages=%d mfma=%d waves=%dx%d group_m=%d xcd_remap=%d grid=%lld threads=%d "
-             "lds=%lld",
+             "lds=%lld part_rows=%d",
              plan->entry->name, c.bm, c.bn, c.bk, c.stages, c.mfma, c.waves_m, c.waves_n, c.group_m, c.xcd_remap,
-             (long long)plan->grid, plan->entry->threads, (long long)plan->entry->lds_bytes);
+             (long long)plan->grid, plan->entry->threads, (long long)plan->entry->lds_bytes, plan->part_rows);
+    return GEMM_OK;
+}
+
+gemm_status gemm_grouped_workspace(const gemm_grouped_plan* plan, size_t* bytes) {
+    if (!plan || !bytes) return fail(GEMM_ERR_INVALID_ARG, "plan or bytes is NULL");
+    *bytes = static_cast<size_t>(plan->max_parts * plan->prob.P * plan->prob.Q) * 4;
     return GEMM_OK;
 }
 
 gemm_status gemm_grouped_run(const gemm_grouped_plan* plan, const void* A, const void* B, const int32_t* offsets,
                              void* D, void* stream) {
+    return gemm_grouped_run_parts(plan, A, B, offsets, D, nullptr, 0, stream);
+}
+
+gemm_status gemm_grouped_run_parts(const gemm_grouped_plan* plan, const void* A, const void* B,
+                                   const int32_t* offsets, void* D, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
     if (!plan) return fail(GEMM_ERR_INVALID_ARG, "plan is NULL");
     const gemm_grouped_problem& p = plan->prob;
     const int64_t dn = d_extent(&p), an = a_extent(&p), bn = b_extent(&p);
@@ -313,8 +413,21 @@ gemm_status gemm_grouped_run(const gemm_grouped_plan* plan, const void* A, const
     if (d.meets(Span(A, an * 2))) return fail(GEMM_ERR_INVALID_ARG, "D overlaps A");
     if (d.meets(Span(B, bn * 2))) return fail(GEMM_ERR_INVALID_ARG, "D overlaps B");
     if (d.meets(Span(offsets, (p.groups + 1) * 4))) return fail(GEMM_ERR_INVALID_ARG, "D overlaps offsets");
-    const dtg::GroupedEntry* e = plan->entry;
-    if (e->loads == dtg::kGroupedDirect && (ia % 16 || ib % 16)) e = plan->fallback;
+    const bool aligned = ia % 16 == 0 && ib % 16 == 0;
+    const bool parts = plan->part_rows > 0 && workspace && aligned;
+    if (workspace) {
+        const size_t need = static_cast<size_t>(plan->max_parts * p.P * p.Q) * 4;
+        if (workspace_bytes < need)
+            return fail(GEMM_ERR_WORKSPACE, "%zu bytes of workspace needed (%zu given)", need, workspace_bytes);
+        if (reinterpret_cast<uintptr_t>(workspace) % 16)
+            return fail(GEMM_ERR_WORKSPACE, "workspace must be 16-byte aligned");
+        const Span w(workspace, static_cast<int64_t>(need));
+        if (w.meets(d) || w.meets(Span(A, an * 2)) || w.meets(Span(B, bn * 2)) ||
+            w.meets(Span(offsets, (p.groups + 1) * 4)))
+            return fail(GEMM_ERR_INVALID_ARG, "the workspace overlaps an operand");
+    }
+    const dtg::GroupedEntry* e = parts ? plan->part_entry : plan->entry;
+    if (e->loads == dtg::kGroupedDirect && !aligned) e = plan->fallback;
     dtg::GroupedArgs a;
     a.A = static_cast<const uint16_t*>(A);
     a.B = static_cast<const uint16_t*>(B);
@@ -336,9 +449,18 @@ gemm_status gemm_grouped_run(const gemm_grouped_plan* plan, const void* A, const
     a.sb_q = p.sb_q;
     a.sd_g = p.sd_g;
     a.sd_r = p.sd_r;
-    const hipError_t err = e->launch(a, e == plan->entry ? plan->grid : grid_of(&p, e),
-                                     static_cast<hipStream_t>(stream));
+    a.longest_first = p.groups <= 64 && p.R / kSortRows >= p.groups;
+    a.part_rows = parts ? plan->part_rows : 0;
+    a.max_parts = static_cast<int32_t>(plan->max_parts);
+    a.parts = static_cast<float*>(workspace);
+    const int64_t grid = parts ? plan->max_parts * a.num_pid_p * a.num_pid_q
+                               : e == plan->entry ? plan->grid : grid_of(&p, e);
+    hipError_t err = e->launch(a, grid, static_cast<hipStream_t>(stream));
     if (err != hipSuccess) return fail(GEMM_ERR_HIP, "launch of %s: %s", e->name, hipGetErrorString(err));
+    if (parts) {
+        err = dtg::launch_sum_parts(a, p.dtype == GEMM_BF16 ? 1 : 0, esz == 4 ? 1 : 0, static_cast<hipStream_t>(stream));
+        if (err != hipSuccess) return fail(GEMM_ERR_HIP, "launch of the parts' sum: %s", hipGetErrorString(err));
+    }
     return GEMM_OK;
 }
 

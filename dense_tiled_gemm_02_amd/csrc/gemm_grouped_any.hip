@@ -18,12 +18,10 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_grouped_rows_any_kernel(Gro
 
 template <int BM, int BN, int BK, int WM, int WN, int MF, int ST, bool BF16, bool O32>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_grouped_reduce_any_kernel(GroupedArgs a) {
-    const int tiles = a.num_pid_p * a.num_pid_q;
-    const int pos = xcd_permute<int>(blockIdx.x, gridDim.x, a.xcds);
-    const int g = pos / tiles;
-    const KArgs p = reduce_args<O32>(a, g);
-    int pid_m, pid_n;
-    grouped_tile<int>(pos - g * tiles, p.num_pid_m, p.num_pid_n, p.group_m, &pid_m, &pid_n);
+    KArgs p;
+    int tile, pid_m, pid_n;
+    if (!reduce_work<O32>(a, &p, &tile)) return;
+    grouped_tile<int>(tile, p.num_pid_m, p.num_pid_n, p.group_m, &pid_m, &pid_n);
     reg_tile<BM, BN, BK, WM, WN, MF, ST, BF16, false, O32>(p, pid_m, pid_n);
 }
 

@@ -9,6 +9,7 @@ const GroupedEntry kTable[] = {
     GROUPED_REDUCE(256, 256, 64, 2, 4, 16, 2),
     GROUPED_REDUCE(128, 256, 64, 2, 4, 16, 3),
     GROUPED_REDUCE(128, 128, 64, 2, 4, 16, 2),
+    GROUPED_REDUCE(128, 128, 32, 2, 2, 16, 2),
     GROUPED_REDUCE(64, 64, 64, 2, 2, 16, 4),
 };
 

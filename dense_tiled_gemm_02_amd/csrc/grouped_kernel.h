@@ -128,12 +128,85 @@ __device__ __forceinline__ KArgs row_args(const GroupedArgs& a, const RowTile& t
     return p;
 }
 
-// One whole product's tile (reduce kind): group, then tile within its P x Q.
-// The contraction runs over the group's rows, so K is the group's length.
+// Parts of a group of `rows` rows; a group without rows is one part (of zeros).
+__device__ __forceinline__ uint32_t group_parts(int rows, int part_rows) {
+    const uint32_t n = (static_cast<uint32_t>(rows) + part_rows - 1) / static_cast<uint32_t>(part_rows);
+    return n > 0 ? n : 1;
+}
+
+// Inclusive scan over the wave.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const uint32_t u = __shfl_up(v, d, 64);
+        if (lane >= d) v += u;
+    }
+    return v;
+}
+
+// Part number `want` of all groups' parts in order: its group and rows.  False
+// past the last one.
+__device__ __forceinline__ bool find_part(const GroupedArgs& a, uint32_t want, int* group, Segment* rows) {
+    const int lane = threadIdx.x & 63;
+    uint32_t before = 0;
+    for (int base = 0; base < a.groups; base += 64) {
+        Segment s = {0, 0};
+        uint32_t n = 0;
+        if (base + lane < a.groups) {
+            s = table_segment(a, base + lane + 1);
+            n = group_parts(s.rows, a.part_rows);
+        }
+        const uint32_t incl = wave_scan(n);
+        const uint64_t past = __ballot(before + incl > want);
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            const uint32_t first = before + __builtin_amdgcn_readlane(incl - n, l);
+            const int lo = __builtin_amdgcn_readlane(s.lo, l), len = __builtin_amdgcn_readlane(s.rows, l);
+            const int skip = static_cast<int>(want - first) * a.part_rows;
+            *group = base + l;
+            rows->lo = lo + skip;
+            rows->rows = len - skip < a.part_rows ? len - skip : a.part_rows;
+            return true;
+        }
+        before += __builtin_amdgcn_readlane(incl, 63);
+    }
+    return false;
+}
+
+// The group that is number `rank` in order of length (up to 64 groups).
+__device__ __forceinline__ int group_of_rank(const GroupedArgs& a, int rank) {
+    const int lane = threadIdx.x & 63;
+    const int rows = lane < a.groups ? table_segment(a, lane + 1).rows : -1;
+    int ahead = 0;
+    for (int j = 0; j < a.groups; ++j) {
+        const int other = __builtin_amdgcn_readlane(rows, j);
+        ahead += other > rows || (other == rows && j < lane);
+    }
+    return __builtin_ctzll(__ballot(lane < a.groups && ahead == rank));
+}
+
+// Workgroup -> (group or part, tile of it).  Where the tiles divide by the
+// dies, each die takes the same share of every group, neighbouring tiles
+// together; in one contiguous range each, the die with the longest group
+// finished last (16384 rows over 8 groups: 415 us).
+__device__ __forceinline__ void reduce_position(const GroupedArgs& a, int* item, int* tile) {
+    const int tiles = a.num_pid_p * a.num_pid_q;
+    const int wg = blockIdx.x;
+    if (a.xcds > 1 && tiles % a.xcds == 0) {
+        const int per = tiles / a.xcds, local = wg / a.xcds;
+        *item = local / per;
+        *tile = wg % a.xcds * per + local % per;
+    } else {
+        *item = wg / tiles;
+        *tile = wg % tiles;
+    }
+}
+
+// A group's product as an ordinary one's arguments (reduce kind): the
+// contraction runs over `rows` rows from `lo` on, D is the group's or the part's.
 template <bool O32>
-__device__ __forceinline__ KArgs reduce_args(const GroupedArgs& a, int g) {
-    Segment s = table_segment(a, g + 1);
-    const int lo = __builtin_amdgcn_readfirstlane(s.lo), rows = __builtin_amdgcn_readfirstlane(s.rows);
+__device__ __forceinline__ KArgs reduce_args(const GroupedArgs& a, int g, int lo, int rows) {
     const int64_t at = static_cast<int64_t>(g) * a.sd_g;
     KArgs p;
     p.A = a.A + static_cast<int64_t>(lo) * a.sa_r;
@@ -180,14 +253,34 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_grouped_rows_kernel(Grouped
         p, whole_tile(t.tile, (p.K + BK - 1) / BK));
 }
 
+// The workgroup's product and tile; false for a workgroup past the last part.
+template <bool O32>
+__device__ __forceinline__ bool reduce_work(const GroupedArgs& a, KArgs* p, int* tile) {
+    int item, g;
+    Segment s;
+    reduce_position(a, &item, tile);
+    if (a.part_rows > 0) {
+        if (!find_part(a, item, &g, &s)) return false;
+        *p = reduce_args<O32>(a, g, s.lo, s.rows);
+        p->D = reinterpret_cast<uint16_t*>(a.parts + static_cast<int64_t>(item) * a.P * a.Q);
+        p->ldd = a.Q;
+        p->C = nullptr;
+        p->has_c = 0;
+    } else {
+        g = a.longest_first ? group_of_rank(a, item) : item;
+        s = table_segment(a, g + 1);
+        *p = reduce_args<O32>(a, g, __builtin_amdgcn_readfirstlane(s.lo), __builtin_amdgcn_readfirstlane(s.rows));
+    }
+    return true;
+}
+
 template <int BM, int BN, int BK, int WM, int WN, int MF, int ST, bool BF16, bool O32>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_grouped_reduce_kernel(GroupedArgs a) {
-    const int tiles = a.num_pid_p * a.num_pid_q;
-    const int pos = xcd_permute<int>(blockIdx.x, gridDim.x, a.xcds);
-    const int g = pos / tiles;
-    const KArgs p = reduce_args<O32>(a, g);
+    KArgs p;
+    int tile;
+    if (!reduce_work<O32>(a, &p, &tile)) return;
     dma_tile<BM, BN, BK, WM, WN, MF, ST, BF16 ? kElBF16 : kElF16, true, false, false, false, O32>(
-        p, whole_tile(pos - g * tiles, (p.K + BK - 1) / BK));
+        p, whole_tile(tile, (p.K + BK - 1) / BK));
 }
 
 template <int BM, int BN, int BK, int WM, int WN, int MF, int ST, bool BF16, bool TB>

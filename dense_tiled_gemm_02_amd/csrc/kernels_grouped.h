@@ -25,6 +25,10 @@ struct GroupedArgs {
     int64_t sa_r, sa_p;     // A element (row, p)
     int64_t sb_g, sb_r, sb_q;  // B element (g, p, q) of the rows kind, (row, q) of the reduce kind
     int64_t sd_g, sd_r;
+    int32_t longest_first;  // reduce kind: groups in order of length
+    int32_t part_rows;      // reduce kind: rows of one part of a group (0: whole groups), part n's
+    int32_t max_parts;      // fp32 P x Q sum at parts + n * P * Q; no increasing
+    float* parts;           // table has more than max_parts
 };
 
 typedef hipError_t (*grouped_launch_fn)(const GroupedArgs& args, int64_t grid, hipStream_t stream);
@@ -47,6 +51,9 @@ struct GroupedEntry {
     grouped_launch_fn launch;
     const char* name;
 };
+
+// D[g] (+)= the sum of the parts of group g in order, for each of the groups.
+hipError_t launch_sum_parts(const GroupedArgs& a, int dtype, int out32, hipStream_t stream);
 
 const GroupedEntry* grouped_rows_table(int* count);
 const GroupedEntry* grouped_reduce_table(int* count);

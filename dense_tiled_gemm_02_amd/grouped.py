@@ -30,6 +30,7 @@ class GroupedPlan:
     def __init__(self, handle, problem):
         self.handle = handle
         self.problem = problem
+        self.workspace = gemm_grouped_workspace(self)
 
     def __del__(self):
         h, self.handle = getattr(self, "handle", None), None
@@ -69,6 +70,17 @@ def gemm_grouped_plan_create_for(problem, info, force=None):
 def gemm_grouped_run(plan, A, B, offsets, D, stream=None):
     """Device addresses (integers or None) and a hipStream_t (or None)."""
     _check(lib().gemm_grouped_run(plan.handle, A, B, offsets, D, stream))
+
+
+def gemm_grouped_workspace(plan):
+    n = ctypes.c_size_t()
+    _check(lib().gemm_grouped_workspace(plan.handle, ctypes.byref(n)))
+    return n.value
+
+
+def gemm_grouped_run_parts(plan, A, B, offsets, D, workspace, workspace_bytes, stream=None):
+    """gemm_grouped_run with a workspace (an address, or None) for the parts of long groups."""
+    _check(lib().gemm_grouped_run_parts(plan.handle, A, B, offsets, D, workspace, workspace_bytes, stream))
 
 
 def gemm_group_rows_workspace(R, groups):
@@ -148,6 +160,15 @@ def _offsets_arg(offsets, groups, device):
         raise ValueError("offsets must be contiguous")
 
 
+def _launch(plan, A, B, offsets, out, stream):
+    if plan.workspace:   # released on return: later work of this stream may reuse it, in order
+        ws = A.new_empty(plan.workspace, dtype=torch.uint8)
+        gemm_grouped_run_parts(plan, A.data_ptr(), B.data_ptr(), offsets.data_ptr(), out.data_ptr(), ws.data_ptr(),
+                               plan.workspace, stream)
+    else:
+        gemm_grouped_run(plan, A.data_ptr(), B.data_ptr(), offsets.data_ptr(), out.data_ptr(), stream)
+
+
 def _run(kind, A, B, offsets, out, groups, P, Q, accumulate, config):
     sa, sb, sd = A.stride(), B.stride(), out.stride()
     key = (A.device.index, kind, A.dtype, out.dtype, accumulate, groups, A.shape[0], P, Q, sa, sb, sd,
@@ -172,8 +193,7 @@ def _run(kind, A, B, offsets, out, groups, P, Q, accumulate, config):
             plan = _plans.get(key)
             if plan is None:
                 plan = _plans[key] = gemm_grouped_plan_create(p, A.device.index, config)
-    gemm_grouped_run(plan, A.data_ptr(), B.data_ptr(), offsets.data_ptr(), out.data_ptr(),
-                     _raw_stream(A.device.index))
+    _launch(plan, A, B, offsets, out, _raw_stream(A.device.index))
     return plan
 
 
@@ -234,7 +254,7 @@ def grouped_wgrad(A, G, offsets, out=None, out_dtype=None, accumulate=False, con
         if hit is not None and _current_device() == hit[0]:
             dev, plan, shape, dtype = hit
             D = A.new_empty(shape, dtype=dtype)
-            gemm_grouped_run(plan, A.data_ptr(), G.data_ptr(), offsets.data_ptr(), D.data_ptr(), _raw_stream(dev))
+            _launch(plan, A, G, offsets, D, _raw_stream(dev))
             return D
     _operands(A, G, 2)
     if A.shape[0] != G.shape[0]:

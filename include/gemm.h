@@ -344,9 +344,21 @@ gemm_status gemm_grouped_plan_launch(const gemm_grouped_plan* plan, int64_t* gri
 gemm_status gemm_grouped_plan_describe(const gemm_grouped_plan* plan, char* buf, size_t len);
 
 /* Enqueue the product on `stream`.  offsets: device, groups + 1 int32.  D may
- * overlap neither A, B nor offsets.  No workspace; capturable in a graph. */
+ * overlap neither A, B nor offsets.  Capturable in a graph.
+ *
+ * Where a weight gradient has few output tiles but many rows, the plan may cut
+ * its groups' rows into parts that run side by side; their fp32 sums go through
+ * a workspace of gemm_grouped_workspace bytes (0: nothing to cut) and are added
+ * in order by a second launch.  gemm_grouped_run never cuts; its result can
+ * differ from gemm_grouped_run_parts' in the sums' rounding, each is
+ * reproducible.  workspace: 16-byte aligned, no preparation, for one run at a
+ * time, overlapping no operand; NULL is gemm_grouped_run. */
 gemm_status gemm_grouped_run(const gemm_grouped_plan* plan, const void* A, const void* B, const int32_t* offsets,
                              void* D, void* stream);
+gemm_status gemm_grouped_workspace(const gemm_grouped_plan* plan, size_t* bytes);
+gemm_status gemm_grouped_run_parts(const gemm_grouped_plan* plan, const void* A, const void* B,
+                                   const int32_t* offsets, void* D, void* workspace, size_t workspace_bytes,
+                                   void* stream);
 
 /* The table and the row order of a grouped product from one group id per row:
  * order (R int32) lists the rows by ascending id, rows of one id in their own
