@@ -308,9 +308,9 @@ def group_rows(ids, groups, stream=None):
 
 
 def _group_rows(ids, groups, device, R, id_bytes, need):
-    offsets = ids.new_empty(groups + 1, dtype=torch.int32)
-    order = ids.new_empty(R, dtype=torch.int32)
-    ws = ids.new_empty(need, dtype=torch.uint8) if need else None
+    # one allocation for the table, the order (16-byte aligned) and the workspace
+    sizes = (groups + 1, (-groups - 1) % 4, R, need // 4)
+    offsets, _, order, ws = ids.new_empty(sum(sizes), dtype=torch.int32).split_with_sizes(sizes)
     gemm_group_rows(ids.data_ptr(), id_bytes, R, groups, offsets.data_ptr(), order.data_ptr(),
                     ws.data_ptr() if need else None, need, _raw_stream(device))
     return offsets, order
