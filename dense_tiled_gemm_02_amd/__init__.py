@@ -166,6 +166,27 @@ def _status_name(s):
         return "status %d" % s
 
 
+_binding = None
+
+
+def binding():
+    """The loaded _binding.so (raises if it is not built)."""
+    global _binding
+    if _binding is None:
+        from importlib import machinery, util
+        path = os.path.join(os.path.dirname(LIB_PATH), "_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError("_binding.so is not built (%s); run "
+                               "'python -m dense_tiled_gemm_02_amd.build'" % path)
+        import torch  # noqa: F401  (its libraries first)
+        lib()
+        loader = machinery.ExtensionFileLoader("_binding", path)
+        mod = util.module_from_spec(util.spec_from_loader("_binding", loader))
+        loader.exec_module(mod)
+        _binding = mod
+    return _binding
+
+
 def _check(status):
     if status != GEMM_OK:
         raise GemmError(status, gemm_last_error())

@@ -1,9 +1,10 @@
-"""Build the HIP library libgemm.so (gfx950) in-tree.
+"""Build the HIP library libgemm.so (gfx950) and the torch binding in-tree.
 
     python -m dense_tiled_gemm_02_amd.build [-j N]
 
 Each HIP/C++ source is compiled with hipcc for gfx950 into an object under
-_build/, then linked into dense_tiled_gemm_02_amd/libgemm.so.  Packed fp32
+_build/, then linked into dense_tiled_gemm_02_amd/libgemm.so; csrc/binding.cpp,
+host code against torch's headers, becomes _binding.so.  Packed fp32
 vector instructions are disabled for device code.  The compiler's resource
 report of every kernel (VGPRs, AGPRs, scratch, spills, LDS, occupancy: its
 kernel-resource-usage remarks) is written to _build/kernel_resources.json with
@@ -24,6 +25,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgemm.so")
+BINDING = os.path.join(PKG, "_binding.so")
 ARCH = "gfx950"
 
 SOURCES = ["api.cpp", "api_mx.cpp", "gemm_tile.hip", "gemm_dma.hip", "gemm_dma_more.hip", "gemm_dma_layouts.hip", "gemm_dma_sk.hip",
@@ -111,6 +113,23 @@ def _link(objs, out, verbose):
     os.replace(tmp, out)
 
 
+def build_binding(verbose=False):
+    """The Python extension of the torch calls (host code only; torch's own
+    libraries are loaded by the time it is)."""
+    import sysconfig
+    import torch
+    root = os.path.dirname(torch.__file__)
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+          "-D_GLIBCXX_USE_CXX11_ABI=%d" % abi, "-isystem", sysconfig.get_paths()["include"], "-isystem",
+          os.path.join(root, "include"), "-isystem", os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include"),
+          os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L" + os.path.join(root, "lib"), "-ltorch_python",
+          "-ltorch_cpu", "-lc10", "-lc10_hip"], verbose)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(verbose=False, jobs=None, asm=None):
     os.makedirs(BUILD, exist_ok=True)
     jobs = jobs or min(8, os.cpu_count() or 1)
@@ -119,7 +138,9 @@ def build(verbose=False, jobs=None, asm=None):
     # the largest sources first, so they start at once
     srcs = sorted(SOURCES, key=lambda f: -os.path.getsize(os.path.join(CSRC, f)))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        binding = ex.submit(build_binding, verbose)
         done = dict(zip(srcs, ex.map(lambda s: _compile(s, verbose, asm), srcs)))
+        binding.result()
     _link([done[s][0] for s in SOURCES], LIB, verbose)
     report = {"sources_sha256": source_digest(), "arch": ARCH,
               "kernels": {k: v for s in SOURCES for k, v in done[s][1].items()}}

@@ -19,7 +19,7 @@ import threading
 import torch
 
 from . import (GEMM_BF16, GEMM_F16, GEMM_GROUPED_OUT_F32, GEMM_GROUPED_OUT_SAME, GEMM_GROUPED_REDUCE,
-               GEMM_GROUPED_ROWS, _check, _force, _i32, _i64, _p, gemm_config, gemm_grouped_problem, lib)
+               GEMM_GROUPED_ROWS, _check, _force, _i32, _i64, _p, binding, gemm_config, gemm_grouped_problem, lib)
 
 _CODES = {torch.float16: GEMM_F16, torch.bfloat16: GEMM_BF16}
 
@@ -99,25 +99,33 @@ def gemm_group_rows(ids, id_bytes, R, groups, offsets, order, workspace=None, wo
 _plans = {}
 _lock = threading.Lock()   # guards _plans
 
-# The plain calls (no out, config or stream) that passed every check, by what
-# the checks look at: the operands' types, shapes, strides and devices.  A call
-# found here goes straight to the launch: 6 us of host time instead of 11,
-# which is what the smallest products take.
-_matmul_calls, _wgrad_calls, _rows_calls = {}, {}, {}
-_MOST_CALLS = 4096
+# The plain calls (no out, config or stream) that passed every check are
+# remembered by _binding.so, by what the checks look at: the operands' types,
+# shapes, strides and devices.  A call found there goes straight to the launch:
+# 4.7 us of host time instead of 11, which is what the smallest products take.
+MATMUL, WGRAD, ROWS, W4 = range(4)   # csrc/binding.cpp
+_call = None
 _raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
 
 
-def _signature(a, b, offsets):
-    return (a.dtype, a.shape, a.stride(), a.get_device(), b.dtype, b.shape, b.stride(), b.get_device(),
-            offsets.dtype, offsets.shape, offsets.stride(), offsets.get_device())
+def _remembered(kind, extra, *tensors):
+    """The call's outputs, or None where it has to be checked first."""
+    global _call
+    if _call is None:
+        _call = binding().call
+    r = _call(kind, extra, *tensors)
+    if type(r) is int:
+        _check(r)
+    return r
 
 
-def _remember(calls, key, value):
-    if len(calls) >= _MOST_CALLS:   # ragged row counts: one entry each
-        calls.clear()
-    calls[key] = value
+def _address(name):
+    return ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value
+
+
+def _remember(kind, plan, run, workspace, sizes, dtype, extra, *tensors):
+    binding().remember(kind, plan, plan.handle.value if plan is not None else 0, _address(run), workspace, sizes,
+                       dtype, extra, tensors)
 
 
 def _need_gpu(device, *named):
@@ -213,14 +221,10 @@ def grouped_matmul(A, B, offsets, out=None, config=None, stream=None):
     float16 or bfloat16; offsets: E + 1 int32 on the GPU, not decreasing.
     config: optional dict of gemm_config fields to force.  Asynchronous on
     `stream` (default: torch's current stream)."""
-    key = None
-    if out is None and config is None and stream is None:
-        key = _signature(A, B, offsets)
-        hit = _matmul_calls.get(key)
-        if hit is not None and _current_device() == hit[0]:
-            dev, plan, shape = hit
-            D = A.new_empty(shape)
-            gemm_grouped_run(plan, A.data_ptr(), B.data_ptr(), offsets.data_ptr(), D.data_ptr(), _raw_stream(dev))
+    plain = out is None and config is None and stream is None
+    if plain:
+        D = _remembered(MATMUL, None, A, B, offsets)
+        if D is not None:
             return D
     _operands(A, B, 3)
     E, K, N = B.shape
@@ -235,8 +239,8 @@ def grouped_matmul(A, B, offsets, out=None, config=None, stream=None):
     def call():
         D = out if out is not None else torch.empty((R, N), dtype=A.dtype, device=A.device)
         plan = _run(GEMM_GROUPED_ROWS, A, B, offsets, D, E, K, N, False, config)
-        if key is not None:
-            _remember(_matmul_calls, key, (A.device.index, plan, (R, N)))
+        if plain:
+            _remember(MATMUL, plan, "gemm_grouped_run_parts", plan.workspace, (R, N), A.dtype, None, A, B, offsets)
         return D
     return _on_stream(call, A.device, stream, (A, B, offsets, out))
 
@@ -247,14 +251,10 @@ def grouped_wgrad(A, G, offsets, out=None, out_dtype=None, accumulate=False, con
     stored N x K is grouped_wgrad(G, A).  out_dtype: the operands' dtype (the
     default) or float32.  An empty group gives zeros.  accumulate: add to `out`
     (E x K x N) instead of overwriting it."""
-    key = None
-    if out is None and config is None and stream is None and not accumulate:
-        key = _signature(A, G, offsets) + (out_dtype,)
-        hit = _wgrad_calls.get(key)
-        if hit is not None and _current_device() == hit[0]:
-            dev, plan, shape, dtype = hit
-            D = A.new_empty(shape, dtype=dtype)
-            _launch(plan, A, G, offsets, D, _raw_stream(dev))
+    plain = out is None and config is None and stream is None and not accumulate
+    if plain:
+        D = _remembered(WGRAD, out_dtype, A, G, offsets)
+        if D is not None:
             return D
     _operands(A, G, 2)
     if A.shape[0] != G.shape[0]:
@@ -275,8 +275,8 @@ def grouped_wgrad(A, G, offsets, out=None, out_dtype=None, accumulate=False, con
     def call():
         D = out if out is not None else torch.empty((E, K, N), dtype=dtype, device=A.device)
         plan = _run(GEMM_GROUPED_REDUCE, A, G, offsets, D, E, K, N, accumulate, config)
-        if key is not None:
-            _remember(_wgrad_calls, key, (A.device.index, plan, (E, K, N), dtype))
+        if plain:
+            _remember(WGRAD, plan, "gemm_grouped_run_parts", plan.workspace, (E, K, N), dtype, out_dtype, A, G, offsets)
         return D
     return _on_stream(call, A.device, stream, (A, G, offsets, out))
 
@@ -286,34 +286,29 @@ def group_rows(ids, groups, stream=None):
     order lists the rows by ascending id, rows of one id in their own order and
     rows whose id is outside [0, groups) last; offsets (groups + 1) holds each
     group's first place in it."""
-    key = None
     if stream is None:
-        key = (ids.dtype, ids.shape, ids.stride(), ids.get_device(), groups)
-        hit = _rows_calls.get(key)
-        if hit is not None and _current_device() == hit[0]:
-            return _group_rows(ids, groups, *hit)
+        pair = _remembered(ROWS, groups, ids)
+        if pair is not None:
+            return pair
     if ids.dtype not in (torch.int32, torch.int64):
         raise TypeError("ids must be int32 or int64, got %s" % ids.dtype)
     if ids.dim() != 1 or (ids.shape[0] > 1 and ids.stride(0) != 1):
         raise ValueError("ids must be one contiguous dimension")
     _need_gpu(ids.device, ("ids", ids))
 
+    R = ids.shape[0]
+
     def call():
-        hit = (ids.device.index, ids.shape[0], ids.element_size(), gemm_group_rows_workspace(ids.shape[0], groups))
-        result = _group_rows(ids, groups, *hit)
-        if key is not None:
-            _remember(_rows_calls, key, hit)
-        return result
+        need = gemm_group_rows_workspace(R, groups)
+        offsets = torch.empty(groups + 1, dtype=torch.int32, device=ids.device)
+        order = torch.empty(R, dtype=torch.int32, device=ids.device)
+        ws = torch.empty(need, dtype=torch.uint8, device=ids.device) if need else None
+        gemm_group_rows(ids.data_ptr(), ids.element_size(), R, groups, offsets.data_ptr(), order.data_ptr(),
+                        ws.data_ptr() if need else None, need, _raw_stream(ids.device.index))
+        if stream is None:
+            _remember(ROWS, None, "gemm_group_rows", need, (groups, R, ids.element_size()), torch.int32, groups, ids)
+        return offsets, order
     return _on_stream(call, ids.device, stream, (ids,))
-
-
-def _group_rows(ids, groups, device, R, id_bytes, need):
-    # one allocation for the table, the order (16-byte aligned) and the workspace
-    sizes = (groups + 1, (-groups - 1) % 4, R, need // 4)
-    offsets, _, order, ws = ids.new_empty(sum(sizes), dtype=torch.int32).split_with_sizes(sizes)
-    gemm_group_rows(ids.data_ptr(), id_bytes, R, groups, offsets.data_ptr(), order.data_ptr(),
-                    ws.data_ptr() if need else None, need, _raw_stream(device))
-    return offsets, order
 
 
 class _GroupedLinear(torch.autograd.Function):

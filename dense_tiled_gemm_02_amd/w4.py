@@ -12,7 +12,7 @@ import threading
 import torch
 
 from . import GEMM_BF16, GEMM_F16, _check, _p, gemm_w4_problem, lib
-from .grouped import _current_device, _need_gpu, _on_stream, _raw_stream, _remember
+from .grouped import W4, _need_gpu, _on_stream, _raw_stream, _remember, _remembered
 
 _CODES = {torch.float16: GEMM_F16, torch.bfloat16: GEMM_BF16}
 
@@ -56,7 +56,6 @@ def gemm_w4_run(plan, X, W, S, Z, expert_ids, Y, stream=None):
 
 _plans = {}
 _lock = threading.Lock()   # guards _plans
-_calls = {}                # plain calls that passed every check, as in grouped.py
 
 
 def w4_matvec(X, W, scale, zeros=None, group=128, experts=None, out=None, stream=None):
@@ -68,19 +67,10 @@ def w4_matvec(X, W, scale, zeros=None, group=128, experts=None, out=None, stream
     scale and zeros then with a leading dimension of experts; a row whose id is
     outside it gives zeros.  group: 32, 64 or 128.  Asynchronous on `stream`
     (default: torch's current stream)."""
-    call_key = None
-    if out is None and stream is None:
-        call_key = (X.dtype, X.shape, X.stride(), X.get_device(), W.dtype, W.shape, W.stride(), W.get_device(),
-                    scale.dtype, scale.shape, scale.stride(), scale.get_device(), group,
-                    zeros is not None and (zeros.dtype, zeros.shape, zeros.stride(), zeros.get_device()),
-                    experts is not None and (experts.dtype, experts.shape, experts.stride(), experts.get_device()))
-        hit = _calls.get(call_key)
-        if hit is not None and _current_device() == hit[0]:
-            dev, plan, shape = hit
-            Y = X.new_empty(shape)
-            gemm_w4_run(plan, X.data_ptr(), W.data_ptr(), scale.data_ptr(),
-                        None if zeros is None else zeros.data_ptr(),
-                        None if experts is None else experts.data_ptr(), Y.data_ptr(), _raw_stream(dev))
+    plain = out is None and stream is None
+    if plain:
+        Y = _remembered(W4, group, X, W, scale, zeros, experts)
+        if Y is not None:
             return Y
     if X.dtype not in _CODES:
         raise TypeError("X must be float16 or bfloat16, got %s" % X.dtype)
@@ -139,8 +129,8 @@ def w4_matvec(X, W, scale, zeros=None, group=128, experts=None, out=None, stream
                     zeros.data_ptr() if zeros is not None else None,
                     experts.data_ptr() if experts is not None else None, Y.data_ptr(),
                     _raw_stream(X.device.index))
-        if call_key is not None:
-            _remember(_calls, call_key, (X.device.index, plan, (M, N)))
+        if plain:
+            _remember(W4, plan, "gemm_w4_run", 0, (M, N), X.dtype, group, X, W, scale, zeros, experts)
         return Y
     if experts is not None and W.shape[0] == 0:   # no matrix: every row is outside
         return out.zero_() if out is not None else torch.zeros((M, N), dtype=X.dtype, device=X.device)
