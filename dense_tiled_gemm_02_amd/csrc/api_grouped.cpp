@@ -40,6 +40,7 @@ gemm_status fail(gemm_status st, const char* fmt, ...) {
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxGroups = 65535;
+constexpr int32_t kFewRows = 16;   // rows of the tile for few rows per group
 constexpr double kMostPartBytes = 256e6;   // of workspace for a gradient's parts
 // mean rows of a group from which the weight gradient takes the longest first
 constexpr int64_t kSortRows = 256;
@@ -140,6 +141,7 @@ const dtg::GroupedEntry* find_entry(const gemm_grouped_problem* p, const gemm_de
     const dtg::GroupedEntry* t = loads == dtg::kGroupedAny   ? dtg::grouped_any_table(&n)
                                  : loads == dtg::kGroupedOdd ? dtg::grouped_odd_table(&n)
                                  : reduce_kind(p)            ? dtg::grouped_reduce_table(&n)
+                                 : w.bm == kFewRows          ? dtg::grouped_few_table(&n)
                                                              : dtg::grouped_rows_table(&n);
     const int dtype = p->dtype == GEMM_BF16 ? 1 : 0, out32 = p->out == GEMM_GROUPED_OUT_F32 ? 1 : 0;
     for (int i = 0; i < n; ++i) {
@@ -217,6 +219,20 @@ void choose_rows_tile(const gemm_grouped_problem* p, const gemm_device_info& dev
     }
 }
 
+// Few rows per group: the waves of a workgroup share out K, 0.5 us per 32 k of
+// each.  Worth it while no CU gets two tiles (16 x 1024 x 512 over 8 groups: 5.2
+// us, 64 x 64 tiles 7.0; 64 x 4096 x 4096 over 8, two tiles to a CU: 70 us and 59).
+bool few_rows(const gemm_grouped_problem* p, const gemm_device_info& dev, const gemm_config& tile) {
+    const double groups = static_cast<double>(p->groups < p->R ? p->groups : p->R);
+    if (groups < 1 || p->R > kFewRows * groups) return false;
+    const double per = static_cast<double>(p->R) / groups / kFewRows + 0.5;
+    const int bn = b_transposed(p) ? 32 : 64;
+    if (groups * (per > 1 ? per : 1) * cdiv(p->Q, bn) > dev.cu_count) return false;
+    const TileCost* t = kRowTiles;
+    while (t->bm != tile.bm || t->bn != tile.bn || t->st != tile.stages) ++t;
+    return 0.5 * cdiv(p->P, 32 * 8) < t->alone * cdiv(p->P, 64);
+}
+
 // Reduce kind: the tile, and whether to cut the groups' rows into parts (few
 // output tiles, many rows: 12000 rows of one 264 x 520 gradient 58 us whole,
 // 25 us in parts of 704).  Lengths vary: the longest group counts 1.5 means.
@@ -285,6 +301,12 @@ gemm_status plan_impl(const gemm_grouped_problem* prob, const gemm_device_info* 
     if (loads == dtg::kGroupedDirect && !forced) {
         if (reduce_kind(prob)) choose_reduce_tile(prob, *dev, &want, &part_rows);
         else choose_rows_tile(prob, *dev, &want);
+        if (!reduce_kind(prob) && few_rows(prob, *dev, want)) {
+            gemm_config few;
+            memset(&few, 0, sizeof few);
+            few.bm = kFewRows;
+            if (find_entry(prob, *dev, loads, few)) want = few;
+        }
     }
     const dtg::GroupedEntry* e = find_entry(prob, *dev, loads, want);
     const dtg::GroupedEntry* any = find_entry(prob, *dev, loose, none);
@@ -449,6 +471,7 @@ gemm_status gemm_grouped_run_parts(const gemm_grouped_plan* plan, const void* A,
     a.sb_q = p.sb_q;
     a.sd_g = p.sd_g;
     a.sd_r = p.sd_r;
+    a.cus = plan->dev.cu_count;
     a.longest_first = p.groups <= 64 && p.R / kSortRows >= p.groups;
     a.part_rows = parts ? plan->part_rows : 0;
     a.max_parts = static_cast<int32_t>(plan->max_parts);

@@ -44,11 +44,11 @@ struct RowTile {
     int tile, tiles;       // position among the segment's tiles, its rows of tiles
 };
 
-// The tile of this workgroup, the same in every wave (no LDS, no barrier):
-// lane l counts the tiles of segment base + l, an inclusive scan over the wave
-// places them.  False for a workgroup past the last tile.
+// Tile number `wg` (a workgroup's own, by default), the same in every wave (no
+// LDS, no barrier): lane l counts the tiles of segment base + l, an inclusive
+// scan over the wave places them.  False past the last tile.
 template <int BM>
-__device__ __forceinline__ bool find_row_tile(const GroupedArgs& a, RowTile* out) {
+__device__ __forceinline__ bool find_row_tile(const GroupedArgs& a, RowTile* out, int wg = blockIdx.x) {
     const int lane = threadIdx.x & 63;
     const int nseg = a.groups + 2;
     auto count = [&](int i, Segment* s) {
@@ -79,8 +79,8 @@ __device__ __forceinline__ bool find_row_tile(const GroupedArgs& a, RowTile* out
     }
     if (total > most) return false;
     const int positions = static_cast<int>(total) * a.num_pid_q;
-    if (static_cast<int>(blockIdx.x) >= positions) return false;
-    const int pos = xcd_permute<int>(blockIdx.x, positions, a.xcds);
+    if (wg >= positions) return false;
+    const int pos = xcd_permute<int>(wg, positions, a.xcds);
     const uint32_t want = pos / a.num_pid_q;   // row of tiles over all segments
     uint32_t before = 0;                        // rows of tiles before this chunk of segments
     for (int base = 0; base < nseg; base += 64) {

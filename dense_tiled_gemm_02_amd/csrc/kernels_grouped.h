@@ -25,6 +25,7 @@ struct GroupedArgs {
     int64_t sa_r, sa_p;     // A element (row, p)
     int64_t sb_g, sb_r, sb_q;  // B element (g, p, q) of the rows kind, (row, q) of the reduce kind
     int64_t sd_g, sd_r;
+    int32_t cus;            // of the device
     int32_t longest_first;  // reduce kind: groups in order of length
     int32_t part_rows;      // reduce kind: rows of one part of a group (0: whole groups), part n's
     int32_t max_parts;      // fp32 P x Q sum at parts + n * P * Q; no increasing
@@ -40,7 +41,7 @@ enum GroupedKind { kGroupedRows = 0, kGroupedReduce = 1 };
 // aligned 16-byte chunks.
 enum GroupedLoads { kGroupedAny = 0, kGroupedDirect = 1, kGroupedOdd = 2 };
 
-// One compiled variant.  tb: B[g] is stored Q x P (rows kind).
+// One compiled variant (bm = 16: few rows per group, waves_n waves over K).  tb: B[g] is stored Q x P (rows kind).
 struct GroupedEntry {
     int32_t kind;
     int32_t bm, bn, bk, stages, mfma, waves_m, waves_n;
@@ -57,6 +58,7 @@ hipError_t launch_sum_parts(const GroupedArgs& a, int dtype, int out32, hipStrea
 
 const GroupedEntry* grouped_rows_table(int* count);
 const GroupedEntry* grouped_reduce_table(int* count);
+const GroupedEntry* grouped_few_table(int* count);
 const GroupedEntry* grouped_odd_table(int* count);
 const GroupedEntry* grouped_any_table(int* count);
 

@@ -338,7 +338,9 @@ void gemm_grouped_plan_destroy(gemm_grouped_plan* plan);
 gemm_status gemm_grouped_plan_config(const gemm_grouped_plan* plan, gemm_config* out);
 
 /* Launch geometry; for GEMM_GROUPED_ROWS the grid covers the most tiles any
- * table can need, and workgroups past the actual number leave at once. */
+ * table can need, and workgroups past the actual number leave at once.  The
+ * 16-row tile (few rows per group) launches at most one workgroup per CU, which
+ * take the grid's tiles in turn. */
 gemm_status gemm_grouped_plan_launch(const gemm_grouped_plan* plan, int64_t* grid, int32_t* threads,
                                      int64_t* lds_bytes);
 gemm_status gemm_grouped_plan_describe(const gemm_grouped_plan* plan, char* buf, size_t len);
