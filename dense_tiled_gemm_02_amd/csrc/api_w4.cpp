@@ -96,17 +96,33 @@ gemm_status plan_impl(const gemm_w4_problem* prob, const gemm_device_info* dev, 
     // rows per pass: two blocks of 16 where a dense batch fills them; a
     // workgroup of an expert sees that expert's rows only
     const int mb = prob->experts == 0 && prob->M > 16 ? 2 : 1;
-    // Columns per workgroup, in blocks of 16.  One block, eight waves, while that
-    // gives no CU two workgroups (16 x 4096 x 4096: 8.2 us, two blocks 9.3); four
-    // blocks, eight waves, where they still reach four CUs in five (16 x 8192 x
-    // 14336: 24 us, two blocks 27; 8 x 8192 x 8192, 128 workgroups: 20 us, two
-    // blocks 15); else two blocks, four waves, two workgroups to a CU.
+    // Columns per workgroup, in blocks of 16, and the waves that share out K.
+    //  one block, eight waves, while that gives no CU two workgroups (16 x 4096
+    //    x 4096: 8.2 us, two blocks 9.3);
+    //  two blocks, one or two waves, where there are four of them to a CU and
+    //    more (30 rows over 60 experts, 1024 x 2786: 20 us, 44 with four waves;
+    //    32 over 16, 4096 x 2048: 26 and 28) or K is short;
+    //  four blocks, eight waves, where they still reach four CUs in five (16 x
+    //    8192 x 14336: 24 us, two blocks 27; 8 x 8192 x 8192, 128 workgroups: 20
+    //    us, two blocks 15);
+    //  else two blocks, four waves, two workgroups to a CU.
     int64_t used = matrices(prob);
     if (used > prob->M) used = prob->M > 0 ? prob->M : 1;
-    const int nb = used * cdiv(prob->N, 16) <= dev->cu_count                                            ? 1
-                   : mb == 1 && prob->group > 32 && 5 * used * cdiv(prob->N, 64) >= 4 * dev->cu_count ? 4
-                                                                                                        : 2;
-    const int waves = mb == 1 && nb != 2 ? 8 : 4;
+    const int64_t cus = dev->cu_count, pairs = used * cdiv(prob->N, 32);
+    int nb = 2, waves = 4;
+    if (used * cdiv(prob->N, 16) <= cus) {
+        nb = 1;
+        waves = mb == 1 ? 8 : 4;
+    } else if (mb == 1) {
+        if (pairs >= 4 * cus) {
+            waves = prob->K <= 1024 ? 1 : 2;
+        } else if (prob->K <= 1024 && 2 * pairs >= 3 * cus) {
+            waves = 2;
+        } else if (prob->group > 32 && 5 * used * cdiv(prob->N, 64) >= 4 * cus) {
+            nb = 4;
+            waves = 8;
+        }
+    }
     int n = 0;
     const dtg::W4Entry* t = dtg::w4_kernel_table(&n);
     const dtg::W4Entry* e = nullptr;

@@ -34,7 +34,9 @@
 // groups of 64 with zero points, 24 us, against 13.7 us for reading W alone in
 // this order of lanes (10.5 us in consecutive 1 KB); 1 x 4096 x 4096 6.6 us.
 // Bound by issue: about 70 vector instructions per 1 KB of W, of which 32
-// unpack the nibbles, and 3 us before the first product.
+// unpack the nibbles, and 3 us before the first product.  With many workgroups
+// those 3 us count most, and one wave with 32 columns to itself wins (30 rows
+// over 60 experts, 1024 x 2786: 20 us, 44 with four waves to 32 columns).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -47,8 +49,6 @@ namespace {
 using namespace dev;
 
 constexpr int kListRows = 256;    // rows gathered per pass over the expert ids
-constexpr int kPanel = 128;       // groups of k whose scales are held in LDS at a time
-constexpr int kPitch = kPanel + 1;   // odd: 16 columns' reads of one group meet no LDS bank twice
 
 // Lowest mantissa bit of the units place of 16.0.
 template <bool BF16> constexpr int kUnits = BF16 ? 3 : 6;
@@ -114,8 +114,13 @@ __device__ __forceinline__ float plain_sum(const uint16_t* x, const uint8_t* w, 
     return y;
 }
 
-template <int NB, int MB, int NWV, int G, bool BF16, bool ZP>
+// PANEL: groups of k whose scales are held in LDS at a time.
+template <int NB, int MB, int NWV, int PANEL, int G, bool BF16, bool ZP>
 __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
+    constexpr int kPanel = PANEL;
+    constexpr int kPitch = PANEL + 1;    // odd: 16 columns' reads of one group meet no LDS bank twice
+    constexpr int LPC = PANEL / 4;       // lanes per column of the table, four groups each
+    constexpr int CPL = 64 / LPC;        // columns per load
     constexpr int NG = 128 / G;          // groups per chunk
     constexpr int UW = NB == 4 ? 2 : 4;  // chunks of W in flight, in registers
     constexpr int UX = 2;                // chunks of X in flight, in LDS
@@ -150,20 +155,20 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
 
     // {scale, offset} of groups [p0, p0 + held) of every column, zeros up to a multiple of 4.
     // In two steps, all loads before the first store: loaded and stored one by
-    // one, the table took half of a wave's time.  Half a wave per column, four
-    // groups per lane.
+    // one, the table took half of a wave's time.
     struct __attribute__((packed, aligned(2))) Loose8 {
         uint32_t v[2];
     };
     struct __attribute__((packed, aligned(1))) Loose4 {
         uint32_t v;
     };
-    const int tcol = wave * CW + (lane >> 5), tgroup = 4 * (lane & 31);   // columns tcol + 2 c, groups tgroup + 0..3
-    uint32_t ts[CW / 2][2], tz[CW / 2];
+    static_assert(CW % CPL == 0, "whole loads of table columns");
+    const int tcol = wave * CW + lane / LPC, tgroup = 4 * (lane % LPC);   // columns tcol + CPL c, groups tgroup + 0..3
+    uint32_t ts[CW / CPL][2], tz[CW / CPL];
     auto load_table = [&](int p0, int held) {
 #pragma unroll
-        for (int c = 0; c < CW / 2; ++c) {
-            const uint32_t n = tcol + 2 * c < cols ? tcol + 2 * c : cols - 1;
+        for (int c = 0; c < CW / CPL; ++c) {
+            const uint32_t n = tcol + CPL * c < cols ? tcol + CPL * c : cols - 1;
             const uint16_t* s = S + static_cast<uint64_t>(n) * static_cast<uint32_t>(a.ss_n) + p0;
             const uint8_t* z = ZP ? Z + static_cast<uint64_t>(n) * static_cast<uint32_t>(a.sz_n) + p0 : nullptr;
             ts[c][0] = ts[c][1] = 0;
@@ -187,8 +192,8 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
     };
     auto store_table = [&](int held) {
 #pragma unroll
-        for (int c = 0; c < CW / 2; ++c) {
-            float2* row = tab + (tcol + 2 * c) * kPitch;
+        for (int c = 0; c < CW / CPL; ++c) {
+            float2* row = tab + (tcol + CPL * c) * kPitch;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (tgroup < held)
@@ -491,9 +496,9 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
     }
 }
 
-template <int NB, int MB, int NWV, int G, bool BF16, bool ZP>
+template <int NB, int MB, int NWV, int PANEL, int G, bool BF16, bool ZP>
 hipError_t launch_w4(const W4Args& a, int64_t tiles, hipStream_t stream) {
-    hipLaunchKernelGGL((gemm_w4_kernel<NB, MB, NWV, G, BF16, ZP>),
+    hipLaunchKernelGGL((gemm_w4_kernel<NB, MB, NWV, PANEL, G, BF16, ZP>),
                        dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(a.num_experts)), dim3(64 * NWV), 0,
                        stream, a);
     return hipGetLastError();
@@ -501,20 +506,23 @@ hipError_t launch_w4(const W4Args& a, int64_t tiles, hipStream_t stream) {
 
 #define DTG_STR2(x) #x
 #define DTG_STR(x) DTG_STR2(x)
-#define W4_ENTRY(NB, MB, NWV, G, BF, ZP)                                                     \
-    {NB, MB, NWV, G, BF, ZP, &launch_w4<NB, MB, NWV, G, (BF != 0), (ZP != 0)>,               \
-     "gemm_w4_kernel<" DTG_STR(NB) "," DTG_STR(MB) "," DTG_STR(NWV) "," DTG_STR(G) "," DTG_STR(BF) "," DTG_STR(ZP) ">"}
+#define W4_ENTRY(NB, MB, NWV, PN, G, BF, ZP)                                                 \
+    {NB, MB, NWV, G, BF, ZP, &launch_w4<NB, MB, NWV, PN, G, (BF != 0), (ZP != 0)>,           \
+     "gemm_w4_kernel<" DTG_STR(NB) "," DTG_STR(MB) "," DTG_STR(NWV) "," DTG_STR(PN) "," DTG_STR(G) "," DTG_STR(BF) "," \
+     DTG_STR(ZP) ">"}
 // (groups of 32 keep twice the scales in registers: four column blocks would spill)
-#define W4_WIDE(NB, MB, NWV)                                                                                     \
-    W4_ENTRY(NB, MB, NWV, 128, 0, 0), W4_ENTRY(NB, MB, NWV, 128, 0, 1), W4_ENTRY(NB, MB, NWV, 128, 1, 0),         \
-    W4_ENTRY(NB, MB, NWV, 128, 1, 1), W4_ENTRY(NB, MB, NWV, 64, 0, 0), W4_ENTRY(NB, MB, NWV, 64, 0, 1),           \
-    W4_ENTRY(NB, MB, NWV, 64, 1, 0), W4_ENTRY(NB, MB, NWV, 64, 1, 1)
-#define W4_GROUPS(NB, MB, NWV)                                                                                   \
-    W4_WIDE(NB, MB, NWV), W4_ENTRY(NB, MB, NWV, 32, 0, 0), W4_ENTRY(NB, MB, NWV, 32, 0, 1),                       \
-    W4_ENTRY(NB, MB, NWV, 32, 1, 0), W4_ENTRY(NB, MB, NWV, 32, 1, 1)
+#define W4_WIDE(NB, MB, NWV, PN)                                                                                 \
+    W4_ENTRY(NB, MB, NWV, PN, 128, 0, 0), W4_ENTRY(NB, MB, NWV, PN, 128, 0, 1),                                   \
+    W4_ENTRY(NB, MB, NWV, PN, 128, 1, 0), W4_ENTRY(NB, MB, NWV, PN, 128, 1, 1),                                   \
+    W4_ENTRY(NB, MB, NWV, PN, 64, 0, 0), W4_ENTRY(NB, MB, NWV, PN, 64, 0, 1),                                     \
+    W4_ENTRY(NB, MB, NWV, PN, 64, 1, 0), W4_ENTRY(NB, MB, NWV, PN, 64, 1, 1)
+#define W4_GROUPS(NB, MB, NWV, PN)                                                                               \
+    W4_WIDE(NB, MB, NWV, PN), W4_ENTRY(NB, MB, NWV, PN, 32, 0, 0), W4_ENTRY(NB, MB, NWV, PN, 32, 0, 1),           \
+    W4_ENTRY(NB, MB, NWV, PN, 32, 1, 0), W4_ENTRY(NB, MB, NWV, PN, 32, 1, 1)
 
 const W4Entry kTable[] = {
-    W4_GROUPS(1, 1, 8), W4_GROUPS(2, 1, 4), W4_WIDE(4, 1, 8), W4_GROUPS(1, 2, 4), W4_GROUPS(2, 2, 4),
+    W4_GROUPS(1, 1, 8, 128), W4_GROUPS(2, 1, 4, 128), W4_WIDE(4, 1, 8, 128),
+    W4_GROUPS(1, 2, 4, 128), W4_GROUPS(2, 2, 4, 128), W4_GROUPS(2, 1, 1, 32), W4_GROUPS(2, 1, 2, 64),
 };
 
 }  // namespace

@@ -96,3 +96,20 @@ def test_padded_and_shifted_operands():
     v, b = weights(w, s, z, G)
     got = w4.w4_matvec(X[:, :K], W[:, :K // 2], S[:, :n], zeros=Z[:, :n], group=G)
     check(got, x.double() @ v.t(), x.double().abs() @ b.t())
+
+
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("M,N,K,E", [(33, 600, 160, 64), (40, 500, 1056, 70), (34, 1000, 4128, 40), (3, 13000, 96, 0),
+                                     (7, 12300, 1024, 0)])
+def test_many_workgroups(M, N, K, E, G):
+    """One and two waves to a workgroup, several panels of their smaller tables."""
+    x, w, s, z = make(M, N, K, G, torch.bfloat16, True, E, M * K)
+    ids = torch.arange(M) % E if E else None
+    got = w4.w4_matvec(x.cuda(), w.cuda(), s.cuda(), zeros=z.cuda(), group=G, experts=None if ids is None else ids.cuda())
+    if not E:
+        v, b = weights(w, s, z, G)
+        check(got, x.double() @ v.t(), x.double().abs() @ b.t())
+    for m in range(M if E else 0):
+        e = int(ids[m])
+        v, b = weights(w[e], s[e], z[e], G)
+        check(got[m], v @ x[m].double(), b @ x[m].double().abs())
