@@ -33,7 +33,7 @@ SOURCES = ["api.cpp", "api_mx.cpp", "gemm_tile.hip", "gemm_dma.hip", "gemm_dma_m
            "gemm_skinny.hip", "gemm_static.hip", "gemm_i8.hip",
            "gemm_mx_direct.hip",
            "api_grouped.cpp", "gemm_grouped_rows.hip", "gemm_grouped_reduce.hip", "gemm_grouped_any.hip",
-           "gemm_grouped_odd.hip", "gemm_grouped_few.hip",
+           "gemm_grouped_odd.hip", "gemm_grouped_few.hip", "gemm_grouped_mixed.hip",
            "sum_parts.hip", "group_rows.hip", "api_w4.cpp", "gemm_w4.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -129,10 +129,18 @@ bool odd_ok(const gemm_grouped_problem* p) {
     return p->sb_q == 1 && p->Q >= 8;
 }
 
+bool mixed(const dtg::GroupedEntry* e) {
+    int n = 0;
+    const dtg::GroupedEntry* t = dtg::grouped_mixed_table(&n);
+    return e >= t && e < t + n;
+}
+
 // Workgroups of a launch: every tile any table can need (see grouped_kernel.h).
-int64_t grid_of(const gemm_grouped_problem* p, const dtg::GroupedEntry* e) {
+int64_t grid_of(const gemm_grouped_problem* p, const dtg::GroupedEntry* e, int64_t cus) {
     if (reduce_kind(p)) return p->groups * cdiv(p->P, e->bm) * cdiv(p->Q, e->bn);
-    return (p->R / e->bm + p->groups + 2) * cdiv(p->Q, e->bn);
+    const int64_t tiles = (p->R / e->bm + p->groups + 2) * cdiv(p->Q, e->bn);
+    // the mixed tiles: two small ones in place of a group's last row of tiles, at most a round in place of others
+    return mixed(e) ? tiles + (p->groups + 2) * cdiv(p->Q, e->bn) + cus : tiles;
 }
 
 const dtg::GroupedEntry* find_entry(const gemm_grouped_problem* p, const gemm_device_info& dev,
@@ -314,7 +322,14 @@ gemm_status plan_impl(const gemm_grouped_problem* prob, const gemm_device_info* 
         return fail(GEMM_ERR_UNSUPPORTED, "no grouped kernel for bm=%d bn=%d bk=%d stages=%d waves=%dx%d mfma=%d on "
                     "these operands within %lld bytes of LDS", want.bm, want.bn, want.bk, want.stages, want.waves_m,
                     want.waves_n, want.mfma, (long long)dev->lds_per_wg);
-    if (grid_of(prob, e) > kMaxDim || grid_of(prob, any) > kMaxDim)
+    // both tile sizes in one launch, where the lanes of a wave hold all segments
+    if (loads == dtg::kGroupedDirect && !reduce_kind(prob) && !forced && e->bm == 256 && prob->groups + 2 <= 64) {
+        int n = 0;
+        const dtg::GroupedEntry* t = dtg::grouped_mixed_table(&n);
+        for (int i = 0; i < n; ++i)
+            if (t[i].dtype == e->dtype && t[i].tb == e->tb) e = &t[i];
+    }
+    if (grid_of(prob, e, dev->cu_count) > kMaxDim || grid_of(prob, any, dev->cu_count) > kMaxDim)
         return fail(GEMM_ERR_UNSUPPORTED, "output too large for one launch");
     gemm_grouped_plan* pl = new (std::nothrow) gemm_grouped_plan;
     if (!pl) return fail(GEMM_ERR_INVALID_ARG, "out of host memory");
@@ -322,7 +337,7 @@ gemm_status plan_impl(const gemm_grouped_problem* prob, const gemm_device_info* 
     pl->dev = *dev;
     pl->entry = e;
     pl->fallback = any;
-    pl->grid = grid_of(prob, e);
+    pl->grid = grid_of(prob, e, dev->cu_count);
     pl->part_entry = nullptr;
     pl->part_rows = 0;
     pl->max_parts = 0;
@@ -477,7 +492,7 @@ gemm_status gemm_grouped_run_parts(const gemm_grouped_plan* plan, const void* A,
     a.max_parts = static_cast<int32_t>(plan->max_parts);
     a.parts = static_cast<float*>(workspace);
     const int64_t grid = parts ? plan->max_parts * a.num_pid_p * a.num_pid_q
-                               : e == plan->entry ? plan->grid : grid_of(&p, e);
+                               : e == plan->entry ? plan->grid : grid_of(&p, e, plan->dev.cu_count);
     hipError_t err = e->launch(a, grid, static_cast<hipStream_t>(stream));
     if (err != hipSuccess) return fail(GEMM_ERR_HIP, "launch of %s: %s", e->name, hipGetErrorString(err));
     if (parts) {

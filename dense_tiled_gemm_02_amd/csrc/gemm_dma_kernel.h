@@ -139,9 +139,10 @@ __device__ __forceinline__ Work slice_work(const KArgs& p) {
 // non-temporal (the variants for a grid of one row of tiles, where each byte
 // of B is read by one workgroup per K slice).  O32: C and D are fp32 (the
 // weight gradients of the products grouped by expert).
+// smem: the ring, ST * (BM + BN) * BK elements of LDS, 1024-byte aligned.
 template <int BM, int BN, int BK, int WM, int WN, int MF, int ST, int EL, bool TA, bool TB, bool XCH = false,
           bool NTB = false, bool O32 = false>
-__device__ __forceinline__ void dma_tile(const KArgs& p, const Work& wk) {
+__device__ __forceinline__ void dma_tile_in(uint16_t* const smem, const KArgs& p, const Work& wk) {
     constexpr bool BF16 = EL == kElBF16;
     constexpr bool I8 = EL == kElI8;
     constexpr int NW = WM * WN;
@@ -163,8 +164,6 @@ __device__ __forceinline__ void dma_tile(const KArgs& p, const Work& wk) {
     // 128 x 128 wave tile) they live in AGPRs, placed there explicitly
     constexpr bool AGPR = FM * FN * AccT<MF>::regs > 128;
     static_assert(!((I8 || O32) && AGPR), "tiles with 32-bit output keep their accumulators in VGPRs");
-
-    __shared__ __attribute__((aligned(1024))) uint16_t smem[ST * (SA + SB)];
 
     int tid = threadIdx.x;
     // Stream-K runs this body in a loop: an opaque lane index keeps the
@@ -857,6 +856,14 @@ __device__ __forceinline__ void dma_tile(const KArgs& p, const Work& wk) {
         }
     }
     }   // 16-bit epilogues
+}
+
+// The same with a ring of its own.
+template <int BM, int BN, int BK, int WM, int WN, int MF, int ST, int EL, bool TA, bool TB, bool XCH = false,
+          bool NTB = false, bool O32 = false>
+__device__ __forceinline__ void dma_tile(const KArgs& p, const Work& wk) {
+    __shared__ __attribute__((aligned(1024))) uint16_t smem[ST * (BM + BN) * BK];
+    dma_tile_in<BM, BN, BK, WM, WN, MF, ST, EL, TA, TB, XCH, NTB, O32>(smem, p, wk);
 }
 
 template <int BM, int BN, int BK, int WM, int WN, int MF, int ST, bool BF16, bool TA, bool TB>

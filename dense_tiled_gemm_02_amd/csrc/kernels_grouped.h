@@ -58,6 +58,7 @@ hipError_t launch_sum_parts(const GroupedArgs& a, int dtype, int out32, hipStrea
 
 const GroupedEntry* grouped_rows_table(int* count);
 const GroupedEntry* grouped_reduce_table(int* count);
+const GroupedEntry* grouped_mixed_table(int* count);
 const GroupedEntry* grouped_few_table(int* count);
 const GroupedEntry* grouped_odd_table(int* count);
 const GroupedEntry* grouped_any_table(int* count);
