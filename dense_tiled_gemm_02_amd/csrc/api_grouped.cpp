@@ -227,7 +227,7 @@ void choose_rows_tile(const gemm_grouped_problem* p, const gemm_device_info& dev
     }
 }
 
-// Few rows per group: the waves of a workgroup share out K, 0.5 us per 32 k of
+// Few rows per group: the waves of a workgroup share out K, 0.35 us per 32 k of
 // each.  Worth it while no CU gets two tiles (16 x 1024 x 512 over 8 groups: 5.2
 // us, 64 x 64 tiles 7.0; 64 x 4096 x 4096 over 8, two tiles to a CU: 70 us and 59).
 bool few_rows(const gemm_grouped_problem* p, const gemm_device_info& dev, const gemm_config& tile) {
@@ -238,7 +238,7 @@ bool few_rows(const gemm_grouped_problem* p, const gemm_device_info& dev, const 
     if (groups * (per > 1 ? per : 1) * cdiv(p->Q, bn) > dev.cu_count) return false;
     const TileCost* t = kRowTiles;
     while (t->bm != tile.bm || t->bn != tile.bn || t->st != tile.stages) ++t;
-    return 0.5 * cdiv(p->P, 32 * 8) < t->alone * cdiv(p->P, 64);
+    return 0.35 * cdiv(p->P, 32 * 8) < t->alone * cdiv(p->P, 64);
 }
 
 // Reduce kind: the tile, and whether to cut the groups' rows into parts (few

@@ -98,13 +98,13 @@ gemm_status plan_impl(const gemm_w4_problem* prob, const gemm_device_info* dev, 
     const int mb = prob->experts == 0 && prob->M > 16 ? 2 : 1;
     // Columns per workgroup, in blocks of 16, and the waves that share out K.
     //  one block, eight waves, while that gives no CU two workgroups (16 x 4096
-    //    x 4096: 8.2 us, two blocks 9.3);
+    //    x 4096: 7.4 us, two blocks 8.5);
     //  two blocks, one or two waves, where there are four of them to a CU and
     //    more (30 rows over 60 experts, 1024 x 2786: 20 us, 44 with four waves;
-    //    32 over 16, 4096 x 2048: 26 and 28) or K is short;
+    //    32 over 16, 4096 x 2048: 25 and 27) or K is short;
     //  four blocks, eight waves, where they still reach four CUs in five (16 x
-    //    8192 x 14336: 24 us, two blocks 27; 8 x 8192 x 8192, 128 workgroups: 20
-    //    us, two blocks 15);
+    //    8192 x 14336: 22 us, two blocks 25; 8 x 8192 x 8192, 128 workgroups: 18
+    //    us, two blocks 14);
     //  else two blocks, four waves, two workgroups to a CU.
     int64_t used = matrices(prob);
     if (used > prob->M) used = prob->M > 0 ? prob->M : 1;

@@ -5,10 +5,11 @@
 // the 32-k chunks of K in turn, each through a private ST-stage LDS ring filled
 // by direct loads (the layouts of the direct tiles, OpShape), so no barrier is
 // needed until the waves' sums meet in LDS, added in wave order.  Bound by
-// latency, about 0.5 us per chunk of a wave and 3 us around them: 16 x 1024 x
+// latency, about 0.35 us per chunk of a wave and 3 us around them: 16 x 1024 x
 // 512 over 8 groups 5.2 us (64 x 64 tiles with one K loop 7.0), 4 x 3880 x 136
-// over 19 groups 11.6 us (16.9).  A deeper ring (6 stages) starts later and
-// gains nothing.
+// over 19 groups 8.8 us (16.9), 1 x 4096 x 4096 10.5 us (17.7).  A deeper ring (6
+// stages) starts later and gains nothing; non-temporal loads of B, which the
+// next step's call reads again, cost 1 x 4096 x 4096 6 us.
 #include "grouped_kernel.h"
 
 namespace dtg {
@@ -67,7 +68,7 @@ __device__ __forceinline__ void few_tile(const KArgs& p, int pid_m, int pid_n) {
 #pragma unroll
         for (int i = 0; i < OB::IW; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void_t*)(sa + OA::SZ + i * 512), 16,
-                                                     b_voff[i] | (k0 + b_k[i] < K ? 0u : kOOB), 0, 0, kNonTemporal);
+                                                     b_voff[i] | (k0 + b_k[i] < K ? 0u : kOOB), 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < OA::IW; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void_t*)(sa + i * 512), 16,

@@ -20,18 +20,20 @@
 // infinite) is summed again term by term.
 //
 // A wave takes chunks of 128 k of 16 NB rows of W: each lane one 16-byte load
-// per 16 rows (row l mod 16, k 32 (l / 16) .. + 31), non-temporal, UW chunks
-// ahead in registers; X comes through a ring in LDS, filled by direct loads;
-// the scales and offsets of the workgroup's columns are converted into an LDS
-// table once.  The order of k inside the instruction is free as long as X
+// per 16 rows (row l mod 16, k 32 (l / 16) .. + 31), UW chunks ahead in
+// registers (cached: non-temporal, the two waves that share each 128-byte line
+// both fetch it, 24 us in place of 22 below); X comes through a ring in LDS,
+// filled by direct loads; the scales and offsets of the workgroup's columns are
+// converted into an LDS table once.  The order of k inside the instruction is free as long as X
 // follows it, so with groups of 128 a lane's four dwords are simply four
 // instructions; for groups of 64 or 32 the dwords are first exchanged between
 // the wave's halves (and quarters) so that every instruction stays inside one
 // group.  The waves of a workgroup take the chunks in turn and their sums are
 // added through LDS in wave order, so a call's result does not depend on timing.
 //
-// Measured (W rotated through 350 MB, past the caches): 16 x 8192 x 14336,
-// groups of 64 with zero points, 24 us, against 13.7 us for reading W alone in
+// Measured (W rotated through 350 MB, past the caches; 19 us from them): 16 x
+// 8192 x 14336,
+// groups of 64 with zero points, 22 us, against 13.0 us for reading W alone in
 // this order of lanes (10.5 us in consecutive 1 KB); 1 x 4096 x 4096 6.6 us.
 // Bound by issue: about 70 vector instructions per 1 KB of W, of which 32
 // unpack the nibbles, and 3 us before the first product.  With many workgroups
@@ -254,7 +256,7 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
                 const uint8_t* wk = W + static_cast<int64_t>(chunk) * 64;
 #pragma unroll
                 for (int j = 0; j < NB; ++j)
-                    d[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wk + woff[j]));
+                    d[j] = *reinterpret_cast<const u32x4*>(wk + woff[j]);
             };
             // The wave's whole chunks of the panel from group p0 on: c0 + wave,
             // c0 + wave + NWV, ... (`mine` of them); W of the first ones is on its
