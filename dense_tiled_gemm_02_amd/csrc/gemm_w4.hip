@@ -24,21 +24,21 @@
 // registers (cached: non-temporal, the two waves that share each 128-byte line
 // both fetch it, 24 us in place of 22 below); X comes through a ring in LDS,
 // filled by direct loads; the scales and offsets of the workgroup's columns are
-// converted into an LDS table once.  The order of k inside the instruction is free as long as X
-// follows it, so with groups of 128 a lane's four dwords are simply four
-// instructions; for groups of 64 or 32 the dwords are first exchanged between
-// the wave's halves (and quarters) so that every instruction stays inside one
-// group.  The waves of a workgroup take the chunks in turn and their sums are
-// added through LDS in wave order, so a call's result does not depend on timing.
+// converted into an LDS table once.  The order of k inside the instruction is
+// free as long as X follows it, so with groups of 128 a lane's four dwords are
+// simply four instructions; for groups of 64 or 32 the dwords are first
+// exchanged between the wave's halves (and quarters) so that every instruction
+// stays inside one group.  The waves of a workgroup take the chunks in turn and
+// their sums are added through LDS in wave order, so a call's result does not
+// depend on timing.
 //
-// Measured (W rotated through 350 MB, past the caches; 19 us from them): 16 x
-// 8192 x 14336,
-// groups of 64 with zero points, 22 us, against 13.0 us for reading W alone in
-// this order of lanes (10.5 us in consecutive 1 KB); 1 x 4096 x 4096 6.6 us.
-// Bound by issue: about 70 vector instructions per 1 KB of W, of which 32
-// unpack the nibbles, and 3 us before the first product.  With many workgroups
-// those 3 us count most, and one wave with 32 columns to itself wins (30 rows
-// over 60 experts, 1024 x 2786: 20 us, 44 with four waves to 32 columns).
+// Measured: 16 x 8192 x 14336, groups of 64 with zero points, 22 us with W from
+// memory (19 us from the caches), against 13.0 us for reading W alone in this
+// order of lanes (10.5 us in consecutive 1 KB); 1 x 4096 x 4096 6.2 us.  Bound
+// by issue: about 70 vector instructions per 1 KB of W, of which 32 unpack the
+// nibbles, and 3 us before the first product.  With many workgroups those 3 us
+// count most, and one wave with 32 columns to itself wins (30 rows over 60
+// experts, 1024 x 2786: 20 us, 44 with four waves to 32 columns).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -124,8 +124,8 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
     constexpr int LPC = PANEL / 4;       // lanes per column of the table, four groups each
     constexpr int CPL = 64 / LPC;        // columns per load
     constexpr int NG = 128 / G;          // groups per chunk
-    constexpr int UW = NB == 4 ? 2 : 4;  // chunks of W in flight, in registers
-    constexpr int UX = 2;                // chunks of X in flight, in LDS
+    constexpr int UW = NB == 4 || (MB == 2 && NWV == 2) ? 2 : 4;   // chunks of W in flight, in registers
+    constexpr int UX = 2;                                         // chunks of X in flight, in LDS
     constexpr int ROWS = 16 * MB;
     constexpr int CW = 16 * NB / NWV;    // columns of the table per wave
     __shared__ float2 tab[16 * NB * kPitch];
@@ -137,9 +137,28 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4;
-    const int e = blockIdx.y;
     const int n0 = blockIdx.x * (16 * NB);
     const int M = a.M, N = a.N, K = a.K;
+    auto id_of = [&](int row) -> int64_t {
+        return a.id_bytes == 8 ? static_cast<const int64_t*>(a.experts)[row]
+                               : static_cast<const int32_t*>(a.experts)[row];
+    };
+    int expert = blockIdx.y;
+    if (a.by_row) {   // more experts than rows, 64 of those at most: the blockIdx.y-th that a row names
+        const int64_t id = lane < M ? id_of(lane) : -1;
+        const bool named = id >= 0 && id < a.num_experts;
+        bool again = false;
+        for (int j = 0; j < M - 1; ++j) {
+            const int other = __builtin_amdgcn_readlane(static_cast<int>(id), j);   // num_experts fits 16 bits
+            again |= named && j < lane && other == static_cast<int>(id) && __builtin_amdgcn_readlane(named, j);
+        }
+        uint64_t first = __ballot(named && !again);
+        if (__popcll(first) <= expert && expert > 0) return;
+        for (int k = 0; k < expert; ++k) first &= first - 1;
+        expert = first ? __builtin_amdgcn_readlane(static_cast<int>(id), __builtin_ctzll(first)) : -1;
+    }
+    // no row names an expert: nothing but the zeros to write
+    const int e = expert < 0 ? 0 : expert;
     const uint8_t* const W = a.W + static_cast<int64_t>(e) * a.sw_e + static_cast<int64_t>(n0) * a.sw_n;
     const uint16_t* const S = a.S + static_cast<int64_t>(e) * a.ss_e + static_cast<int64_t>(n0) * a.ss_n;
     const uint8_t* const Z = ZP ? a.Z + static_cast<int64_t>(e) * a.sz_e + static_cast<int64_t>(n0) * a.sz_n : nullptr;
@@ -230,15 +249,13 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
                 for (int r = first; r < end; r += 64) {
                     const int row = r + lane;
                     int64_t id = -1;
-                    if (row < end)
-                        id = a.id_bytes == 8 ? static_cast<const int64_t*>(a.experts)[row]
-                                             : static_cast<const int32_t*>(a.experts)[row];
-                    const bool mine = row < end && id == e;
+                    if (row < end) id = id_of(row);
+                    const bool mine = row < end && id == expert && expert >= 0;
                     const uint64_t hits = __ballot(mine);
                     if (mine) list[n + __popcll(hits & ((uint64_t(1) << lane) - 1))] = row;
                     n += __popcll(hits);
-                    // rows of no expert are zeros, written by the first expert's workgroups
-                    if (e == 0 && row < end && (id < 0 || id >= a.num_experts))
+                    // rows of no expert are zeros, written by the first workgroups
+                    if (blockIdx.y == 0 && row < end && (id < 0 || id >= a.num_experts))
                         for (int c = 0; c < cols; ++c) a.Y[static_cast<int64_t>(row) * a.sy + n0 + c] = 0;
                 }
                 if (lane == 0) listed = n;
@@ -501,7 +518,7 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
 template <int NB, int MB, int NWV, int PANEL, int G, bool BF16, bool ZP>
 hipError_t launch_w4(const W4Args& a, int64_t tiles, hipStream_t stream) {
     hipLaunchKernelGGL((gemm_w4_kernel<NB, MB, NWV, PANEL, G, BF16, ZP>),
-                       dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(a.num_experts)), dim3(64 * NWV), 0,
+                       dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(a.by_row ? a.M : a.num_experts)), dim3(64 * NWV), 0,
                        stream, a);
     return hipGetLastError();
 }
@@ -524,7 +541,7 @@ hipError_t launch_w4(const W4Args& a, int64_t tiles, hipStream_t stream) {
 
 const W4Entry kTable[] = {
     W4_GROUPS(1, 1, 8, 128), W4_GROUPS(2, 1, 4, 128), W4_WIDE(4, 1, 8, 128),
-    W4_GROUPS(1, 2, 4, 128), W4_GROUPS(2, 2, 4, 128), W4_GROUPS(2, 1, 1, 32), W4_GROUPS(2, 1, 2, 64),
+    W4_GROUPS(1, 2, 4, 128), W4_GROUPS(2, 2, 4, 128), W4_GROUPS(2, 2, 2, 64), W4_GROUPS(2, 1, 1, 32), W4_GROUPS(2, 1, 2, 64),
 };
 
 }  // namespace

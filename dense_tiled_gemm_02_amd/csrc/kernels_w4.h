@@ -19,6 +19,7 @@ struct W4Args {
     int32_t M, N, K;
     int32_t num_experts;    // 1 without experts
     int32_t id_bytes;       // 4 or 8
+    int32_t by_row;         // workgroups for each row's expert in place of each expert (M <= 64)
     int64_t sx, sy;
     int64_t sw_n, sw_e, ss_n, ss_e, sz_n, sz_e;
 };

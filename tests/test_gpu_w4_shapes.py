@@ -113,3 +113,28 @@ def test_many_workgroups(M, N, K, E, G):
         e = int(ids[m])
         v, b = weights(w[e], s[e], z[e], G)
         check(got[m], v @ x[m].double(), b @ x[m].double().abs())
+
+
+@pytest.mark.parametrize("wide", [torch.int32, torch.int64])
+@pytest.mark.parametrize("ids", [[3], [-1], [5, 5, 5], [9, 2, 9, -4, 70, 2], [-1, 80, 2 ** 20], list(range(63, -1, -1)),
+                                 [7] * 33 + [65, 0] + [7] * 29], ids=lambda x: "%dr" % len(x))
+def test_more_experts_than_rows(ids, wide):
+    """Workgroups follow the experts that the rows name; rows outside are zeros."""
+    M, N, K, E, G = len(ids), 70, 160, 66, 32
+    x, w, s, z = make(M, N, K, G, torch.float16, True, E, M)
+    got = w4.w4_matvec(x.cuda(), w.cuda(), s.cuda(), zeros=z.cuda(), group=G, experts=torch.tensor(ids, dtype=wide).cuda(),
+                       out=torch.full((M, N), 7.0, dtype=torch.float16, device="cuda"))
+    for m, e in enumerate(ids):
+        if 0 <= e < E:
+            v, b = weights(w[e], s[e], z[e], G)
+            check(got[m], v @ x[m].double(), b @ x[m].double().abs())
+        else:
+            assert (got[m] == 0).all()
+
+
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("M,N,K", [(17, 8300, 160), (32, 8200, 1152)])
+def test_two_row_blocks_over_many_columns(M, N, K, G):
+    x, w, s, z = make(M, N, K, G, torch.bfloat16, True, 0, N)
+    v, b = weights(w, s, z, G)
+    check(w4.w4_matvec(x.cuda(), w.cuda(), s.cuda(), zeros=z.cuda(), group=G), x.double() @ v.t(), x.double().abs() @ b.t())
