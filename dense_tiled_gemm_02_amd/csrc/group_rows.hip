@@ -17,7 +17,7 @@
 // of the blocks before it for itself.  Past kSelfScan blocks that sum would
 // outgrow the placement, and a launch between them scans the counts.
 // Bound by latency, not bytes: 131072 ids over 128 groups, 1 MB, take 9 us
-// (with the scan launch 14.7).
+// (with the scan launch and one placing workgroup per count 14.7).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -172,18 +172,24 @@ __global__ __launch_bounds__(kThreads) void group_scan_kernel(int32_t* counts, i
     if (c < classes) offsets[c] = base;
 }
 
+// kSubs workgroups place the rows of one counting block, each its share of
+// kThreads rows: it counts the shares before its own itself, and its own in one
+// step of 64 rows per wave (with one workgroup per block 7.5 us, so 6.4).
 // SCANNED: the counts are already sums over earlier blocks, and offsets written.
+constexpr int kSubs = kRowsPerBlock / kThreads;
+
 template <typename ID, bool SCANNED>
 __global__ __launch_bounds__(kThreads) void group_place_kernel(const ID* ids, int64_t R, int groups,
                                                                const int32_t* counts, int blocks, int32_t* offsets,
                                                                int32_t* order) {
     __shared__ int before[kClasses], all[kClasses], waves[kWaves];
-    const int classes = groups + 1, here = blockIdx.x;
-    const int64_t first = static_cast<int64_t>(here) * kRowsPerBlock;
+    const int classes = groups + 1, here = blockIdx.x / kSubs, sub = blockIdx.x % kSubs;
+    const int64_t block0 = static_cast<int64_t>(here) * kRowsPerBlock, first = block0 + sub * kThreads;
+    if (first >= R) return;
     // the counts of all blocks, HELD of them in flight per thread while the rows are counted
     constexpr int HELD = 8;
     const int cells = blocks * classes;
-    int v[HELD];
+    int v[HELD], earlier[kSubs - 1];
     auto fetch = [&](int i0) {
 #pragma unroll
         for (int u = 0; u < HELD; ++u) {
@@ -192,11 +198,16 @@ __global__ __launch_bounds__(kThreads) void group_place_kernel(const ID* ids, in
         }
     };
     auto prepare = [&] {
-        if constexpr (SCANNED) return;
-        fetch(threadIdx.x);
+        if constexpr (!SCANNED) fetch(threadIdx.x);
+#pragma unroll
+        for (int u = 0; u < kSubs - 1; ++u)   // whole shares: this one starts before R
+            earlier[u] = u < sub ? class_of(ids, block0 + u * kThreads + threadIdx.x, groups) : -1;
         for (int i = threadIdx.x; i < classes; i += kThreads) before[i] = all[i] = 0;
     };
     auto gather = [&] {   // integer sums, in any order
+#pragma unroll
+        for (int u = 0; u < kSubs - 1; ++u)
+            if (earlier[u] >= 0) atomicAdd(&before[earlier[u]], 1);
         if constexpr (SCANNED) return;
         for (int i0 = threadIdx.x; i0 < cells; i0 += HELD * kThreads) {
             if (i0 >= kThreads) fetch(i0);
@@ -212,13 +223,12 @@ __global__ __launch_bounds__(kThreads) void group_place_kernel(const ID* ids, in
     };
     auto place = [&](int tid, int) {
         if constexpr (SCANNED)
-            return tid < classes ? counts[static_cast<int64_t>(here) * classes + tid] + offsets[tid] : 0;
+            return tid < classes ? counts[static_cast<int64_t>(here) * classes + tid] + offsets[tid] + before[tid] : 0;
         const int base = block_exclusive(tid < classes ? all[tid] : 0, waves);
-        if (here == 0 && tid < classes) offsets[tid] = base;
+        if (blockIdx.x == 0 && tid < classes) offsets[tid] = base;
         return base + (tid < classes ? before[tid] : 0);
     };
-    place_rows<kRowsPerBlock / kThreads>(ids, first, first + kRowsPerBlock < R ? first + kRowsPerBlock : R,
-                                         kRowsPerBlock / kWaves, groups, order, prepare, gather, place);
+    place_rows<1>(ids, first, first + kThreads < R ? first + kThreads : R, 64, groups, order, prepare, gather, place);
 }
 
 template <typename ID>
@@ -237,12 +247,12 @@ hipError_t launch_ids(const ID* ids, int64_t R, int32_t groups, int32_t* offsets
     const unsigned blocks = static_cast<unsigned>((R + kRowsPerBlock - 1) / kRowsPerBlock);
     hipLaunchKernelGGL(group_count_kernel<ID>, dim3(blocks), dim3(kThreads), 0, stream, ids, R, groups, counts);
     if (blocks <= kSelfScan) {
-        hipLaunchKernelGGL((group_place_kernel<ID, false>), dim3(blocks), dim3(kThreads), 0, stream, ids, R, groups,
+        hipLaunchKernelGGL((group_place_kernel<ID, false>), dim3(blocks * kSubs), dim3(kThreads), 0, stream, ids, R, groups,
                            counts, static_cast<int>(blocks), offsets, order);
     } else {
         hipLaunchKernelGGL(group_scan_kernel, dim3(1), dim3(kThreads), 0, stream, counts, static_cast<int>(blocks),
                            groups, offsets);
-        hipLaunchKernelGGL((group_place_kernel<ID, true>), dim3(blocks), dim3(kThreads), 0, stream, ids, R, groups,
+        hipLaunchKernelGGL((group_place_kernel<ID, true>), dim3(blocks * kSubs), dim3(kThreads), 0, stream, ids, R, groups,
                            counts, static_cast<int>(blocks), offsets, order);
     }
     return hipGetLastError();
