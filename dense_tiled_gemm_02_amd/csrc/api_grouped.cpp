@@ -40,7 +40,7 @@ gemm_status fail(gemm_status st, const char* fmt, ...) {
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxGroups = 65535;
-constexpr int32_t kFewRows = 16;   // rows of the tile for few rows per group
+constexpr int32_t kFewRows = 16, kFewK = 32;   // the smaller tile for few rows per group; the k chunk of both
 constexpr double kMostPartBytes = 256e6;   // of workspace for a gradient's parts
 // mean rows of a group from which the weight gradient takes the longest first
 constexpr int64_t kSortRows = 256;
@@ -149,7 +149,7 @@ const dtg::GroupedEntry* find_entry(const gemm_grouped_problem* p, const gemm_de
     const dtg::GroupedEntry* t = loads == dtg::kGroupedAny   ? dtg::grouped_any_table(&n)
                                  : loads == dtg::kGroupedOdd ? dtg::grouped_odd_table(&n)
                                  : reduce_kind(p)            ? dtg::grouped_reduce_table(&n)
-                                 : w.bm == kFewRows          ? dtg::grouped_few_table(&n)
+                                 : w.bm == kFewRows || w.bk == kFewK ? dtg::grouped_few_table(&n)
                                                              : dtg::grouped_rows_table(&n);
     const int dtype = p->dtype == GEMM_BF16 ? 1 : 0, out32 = p->out == GEMM_GROUPED_OUT_F32 ? 1 : 0;
     for (int i = 0; i < n; ++i) {
@@ -228,17 +228,30 @@ void choose_rows_tile(const gemm_grouped_problem* p, const gemm_device_info& dev
 }
 
 // Few rows per group: the waves of a workgroup share out K, 0.35 us per 32 k of
-// each.  Worth it while no CU gets two tiles (16 x 1024 x 512 over 8 groups: 5.2
-// us, 64 x 64 tiles 7.0; 64 x 4096 x 4096 over 8, two tiles to a CU: 70 us and 59).
-bool few_rows(const gemm_grouped_problem* p, const gemm_device_info& dev, const gemm_config& tile) {
+// each; 16-row tiles to a mean of 16 rows a group, 64-row ones to 48 (a longer
+// group's second tile reads B[g] again).  Worth it while no CU gets two tiles (16
+// x 1024 x 512 over 8 groups: 5.2 us, 64 x 64 tiles 7.0; 46 x 2184 x 736 over 2:
+// 7.9 and 11.3; 64 x 4096 x 4096 over 8, two tiles to a CU: 70 and 59).  nullptr
+// where it is not.
+const dtg::GroupedEntry* few_rows(const gemm_grouped_problem* p, const gemm_device_info& dev, const gemm_config& tile) {
     const double groups = static_cast<double>(p->groups < p->R ? p->groups : p->R);
-    if (groups < 1 || p->R > kFewRows * groups) return false;
-    const double per = static_cast<double>(p->R) / groups / kFewRows + 0.5;
-    const int bn = b_transposed(p) ? 32 : 64;
-    if (groups * (per > 1 ? per : 1) * cdiv(p->Q, bn) > dev.cu_count) return false;
-    const TileCost* t = kRowTiles;
-    while (t->bm != tile.bm || t->bn != tile.bn || t->st != tile.stages) ++t;
-    return 0.35 * cdiv(p->P, 32 * 8) < t->alone * cdiv(p->P, 64);
+    if (groups < 1) return nullptr;
+    const double mean = static_cast<double>(p->R) / groups;
+    double alone = 0.0;   // stays 0, and nothing is chosen, where no whole tile fits the device
+    for (const TileCost& t : kRowTiles)
+        if (t.bm == tile.bm && t.bn == tile.bn && t.st == tile.stages) alone = t.alone;
+    int n = 0;
+    const dtg::GroupedEntry* few = dtg::grouped_few_table(&n);
+    for (int i = 0; i < n; ++i) {
+        const dtg::GroupedEntry& e = few[i];
+        if (e.dtype != (p->dtype == GEMM_BF16 ? 1 : 0) || e.tb != (b_transposed(p) ? 1 : 0) ||
+            e.lds_bytes > dev.lds_per_wg || mean > (e.bm == kFewRows ? kFewRows : 48))
+            continue;
+        const double per = mean / e.bm + 0.5;
+        if (groups * (per > 1 ? per : 1) * cdiv(p->Q, e.bn) > dev.cu_count) continue;
+        if (0.35 * cdiv(p->P, kFewK * e.waves_n) < alone * cdiv(p->P, 64)) return &e;
+    }
+    return nullptr;
 }
 
 // Reduce kind: the tile, and whether to cut the groups' rows into parts (few
@@ -306,17 +319,13 @@ gemm_status plan_impl(const gemm_grouped_problem* prob, const gemm_device_info* 
     const dtg::GroupedLoads loose = odd_ok(prob) ? dtg::kGroupedOdd : dtg::kGroupedAny;
     const dtg::GroupedLoads loads = vec_ok(prob) ? dtg::kGroupedDirect : loose;
     int32_t part_rows = 0;
+    const dtg::GroupedEntry* few = nullptr;
     if (loads == dtg::kGroupedDirect && !forced) {
         if (reduce_kind(prob)) choose_reduce_tile(prob, *dev, &want, &part_rows);
         else choose_rows_tile(prob, *dev, &want);
-        if (!reduce_kind(prob) && few_rows(prob, *dev, want)) {
-            gemm_config few;
-            memset(&few, 0, sizeof few);
-            few.bm = kFewRows;
-            if (find_entry(prob, *dev, loads, few)) want = few;
-        }
+        if (!reduce_kind(prob)) few = few_rows(prob, *dev, want);
     }
-    const dtg::GroupedEntry* e = find_entry(prob, *dev, loads, want);
+    const dtg::GroupedEntry* e = few ? few : find_entry(prob, *dev, loads, want);
     const dtg::GroupedEntry* any = find_entry(prob, *dev, loose, none);
     if (!e || !any)
         return fail(GEMM_ERR_UNSUPPORTED, "no grouped kernel for bm=%d bn=%d bk=%d stages=%d waves=%dx%d mfma=%d on "

@@ -339,7 +339,7 @@ gemm_status gemm_grouped_plan_config(const gemm_grouped_plan* plan, gemm_config*
 
 /* Launch geometry; for GEMM_GROUPED_ROWS the grid covers the most tiles any
  * table can need, and workgroups past the actual number leave at once.  The
- * 16-row tile (few rows per group) launches at most one workgroup per CU, which
+ * tiles for few rows per group (bk 32) launch at most one workgroup per CU, which
  * take the grid's tiles in turn. */
 gemm_status gemm_grouped_plan_launch(const gemm_grouped_plan* plan, int64_t* grid, int32_t* threads,
                                      int64_t* lds_bytes);
@@ -386,7 +386,7 @@ gemm_status gemm_group_rows_workspace(int64_t R, int64_t groups, size_t* bytes);
  * Every finite output is within
  *     ulp_out + 2^-20 * sum_k 31 |X[m, k] s|
  * of the exact value (the sums run over q + 16 and are corrected: 31 bounds
- * that offset's part).  Bitwise reproducible for a fixed plan. */
+ * that offset's part; with zero points above 15, 31 + z takes its place).  Bitwise reproducible for a fixed plan. */
 typedef struct gemm_w4_problem {
     int64_t M, N, K, group;     /* K a multiple of 32 */
     int64_t experts;            /* 0: one matrix for every row; at most 65535 */
