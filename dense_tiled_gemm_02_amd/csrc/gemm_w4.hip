@@ -444,7 +444,8 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
                     load_w(w[V], c0 + at(i + UW));
                 };
                 if (mine > 0) {
-                    wait_vm<4 * MB>();
+                    // both chunks of X: fewer loads follow the second one here than the count in step() allows for
+                    wait_vm<0>();
                     fetch(std::integral_constant<int, 0>{}, f[0], at(0) * NG);
                     landed(f[0]);
                     load_x(0, c0 + at(2));
