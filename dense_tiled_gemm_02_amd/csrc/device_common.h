@@ -189,6 +189,12 @@ __device__ __forceinline__ u32x2 lds_read8(uint32_t addr) {
     return v;
 }
 template <int OFF>
+__device__ __forceinline__ uint32_t lds_read4(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ds_read_b32 %0, %1 offset:%2" : "=v"(v) : "v"(addr), "i"(OFF));
+    return v;
+}
+template <int OFF>
 __device__ __forceinline__ u32x2 lds_read8_any(uint32_t addr) {
     if constexpr (OFF < 65536)
         return lds_read8<OFF>(addr);

@@ -32,11 +32,17 @@
 // their sums are added through LDS in wave order, so a call's result does not
 // depend on timing.
 //
-// Measured: 16 x 8192 x 14336, groups of 64 with zero points, 22 us with W from
-// memory (19 us from the caches), against 13.0 us for reading W alone in this
-// order of lanes (10.5 us in consecutive 1 KB); 1 x 4096 x 4096 6.2 us.  Bound
-// by issue: about 70 vector instructions per 1 KB of W, of which 32 unpack the
-// nibbles, and 3 us before the first product.  With many workgroups those 3 us
+// Blocks of up to 4 rows (a token, or the few rows of one of many experts) load
+// and keep a quarter of X, four chunks ahead like W: 1 x 4096 x 4096 6.1 -> 5.6
+// us, 32 rows over 16 experts, 4096 x 2048, groups of 32 24 -> 21 us (eight
+// chunks ahead: 22).
+//
+// Measured: 16 x 8192 x 14336, groups of 64 with zero points, 20.5 us with W from
+// memory (18.2 us from the caches), against 13.0 us for reading W alone in this
+// order of lanes (10.5 us in consecutive 1 KB); 1 x 4096 x 4096 5.6 us.  Bound by
+// the loads that two waves per SIMD keep in flight (half of a wave's cycles
+// wait) and by 3 us before the first product; vector instructions, about 70 per
+// 1 KB of W, issue in a third of the cycles.  With many workgroups those 3 us
 // count most, and one wave with 32 columns to itself wins (30 rows over 60
 // experts, 1024 x 2786: 20 us, 44 with four waves to 32 columns).
 #include <hip/hip_runtime.h>
@@ -96,6 +102,13 @@ constexpr int step_k(int t) {
     return G == 128 ? 8 * t : G == 64 ? 64 * (t >> 1) + 8 * (t & 1) : 32 * t;
 }
 
+// Of a chunk of X with 4 rows, piece p of row r sits at p ^ few_place(r): the 16
+// pieces that one instruction's lanes read meet no LDS bank twice.
+template <int G>
+__device__ __forceinline__ int few_place(int r) {
+    return G == 128 ? r : G == 64 ? (r & 1) | (r & 2) << 2 : 4 * r;
+}
+
 // The sum of one output by the formula, term by term in fp32: for outputs
 // that the offset form leaves infinite or NaN.
 template <int G, bool BF16, bool ZP>
@@ -116,19 +129,21 @@ __device__ __forceinline__ float plain_sum(const uint16_t* x, const uint8_t* w, 
     return y;
 }
 
-// PANEL: groups of k whose scales are held in LDS at a time.
+// PANEL: groups of k whose scales and zero points are held in LDS at a time.
 template <int NB, int MB, int NWV, int PANEL, int G, bool BF16, bool ZP>
 __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
-    constexpr int kPanel = PANEL;
-    constexpr int kPitch = PANEL + 1;    // odd: 16 columns' reads of one group meet no LDS bank twice
-    constexpr int LPC = PANEL / 4;       // lanes per column of the table, four groups each
+    constexpr int kPanel = !ZP && PANEL < 128 ? 2 * PANEL : PANEL;   // without zero points the table holds scales alone
+    constexpr int kPitch = kPanel + 1;   // odd: 16 columns' reads of one group meet no LDS bank twice
+    constexpr int LPC = kPanel / 4;      // lanes per column of the table, four groups each
+    typedef std::conditional_t<ZP, float2, float> Entry;
+    typedef std::conditional_t<ZP, u32x2, uint32_t> Scale;
     constexpr int CPL = 64 / LPC;        // columns per load
     constexpr int NG = 128 / G;          // groups per chunk
     constexpr int UW = NB == 4 || (MB == 2 && NWV == 2) ? 2 : 4;   // chunks of W in flight, in registers
-    constexpr int UX = 2;                                         // chunks of X in flight, in LDS
+    constexpr int UX = 2;                                         // chunks of X in flight, in LDS (16 MB rows each)
     constexpr int ROWS = 16 * MB;
     constexpr int CW = 16 * NB / NWV;    // columns of the table per wave
-    __shared__ float2 tab[16 * NB * kPitch];
+    __shared__ Entry tab[16 * NB * kPitch];
     __shared__ __attribute__((aligned(1024))) uint16_t xring[NWV * UX * MB * 2048];
     __shared__ int list[kListRows];
     __shared__ int listed;
@@ -147,11 +162,13 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
     if (a.by_row) {   // more experts than rows, 64 of those at most: the blockIdx.y-th that a row names
         const int64_t id = lane < M ? id_of(lane) : -1;
         const bool named = id >= 0 && id < a.num_experts;
-        bool again = false;
-        for (int j = 0; j < M - 1; ++j) {
-            const int other = __builtin_amdgcn_readlane(static_cast<int>(id), j);   // num_experts fits 16 bits
-            again |= named && j < lane && other == static_cast<int>(id) && __builtin_amdgcn_readlane(named, j);
+        uint64_t same = __ballot(named);   // the rows of this lane's id, one bit of the ids at a time
+        for (int b = 0; (a.num_experts - 1) >> b; ++b) {
+            const bool bit = (id >> b) & 1;
+            const uint64_t set = __ballot(bit);
+            same &= bit ? set : ~set;
         }
+        const bool again = (same & ((uint64_t(1) << lane) - 1)) != 0;
         uint64_t first = __ballot(named && !again);
         if (__popcll(first) <= expert && expert > 0) return;
         for (int k = 0; k < expert; ++k) first &= first - 1;
@@ -214,23 +231,20 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
     auto store_table = [&](int held) {
 #pragma unroll
         for (int c = 0; c < CW / CPL; ++c) {
-            float2* row = tab + (tcol + CPL * c) * kPitch;
+            Entry* row = tab + (tcol + CPL * c) * kPitch;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (tgroup < held)
-                    row[tgroup + i] = float2{widen<BF16>(static_cast<uint16_t>(ts[c][i / 2] >> (16 * (i % 2)))),
-                                             16.0f + static_cast<float>((tz[c] >> (8 * i)) & 255u)};
+                if (tgroup < held) {
+                    const float scale = widen<BF16>(static_cast<uint16_t>(ts[c][i / 2] >> (16 * (i % 2))));
+                    if constexpr (ZP) row[tgroup + i] = float2{scale, 16.0f + static_cast<float>((tz[c] >> (8 * i)) & 255u)};
+                    else row[tgroup + i] = scale;
+                }
         }
     };
     int in_table = -1;   // first group of the table's panel
     float* const red = reinterpret_cast<float*>(xring);
     uint16_t* const xwave = xring + wave * UX * MB * 2048;
-    uint32_t xaddr[4];   // this lane's pieces of X: instruction row lane % 16
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-        xaddr[t] = lds_addr(xwave) + (lane & 15) * 256 +
-                   (((quarter_k<G>(g) + step_k<G>(t)) / 8) ^ (lane & 15)) * 16;
-    const uint32_t tab_addr = lds_addr(reinterpret_cast<const uint16_t*>(tab)) + (lane & 15) * (kPitch * 8);
+    const uint32_t tab_addr = lds_addr(reinterpret_cast<const uint16_t*>(tab)) + (lane & 15) * (kPitch * sizeof(Entry));
 
     uint32_t mask = 0x000F000Fu << kUnits<BF16>, sixteen = BF16 ? 0x41804180u : 0x4C004C00u;
     asm volatile("" : "+s"(mask), "+v"(sixteen));
@@ -267,8 +281,14 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
         }
         auto row_of = [&](int i) { return a.experts ? list[i] : first + i; };
 
-        for (int m0 = 0; m0 < rows; m0 += ROWS) {
-            u32x4 w[UW][NB];
+        // One block of rows.  FEW (4 rows or less of a block of 16): X's chunk is 1 KB,
+        // a row from each quarter of a wave's load, in place of 4 KB of which 3 repeat
+        // the last row, and the ring holds as many chunks of it as of W.
+        auto block = [&](auto few_tag, int m0) {
+            constexpr bool FEW = decltype(few_tag)::value;
+            constexpr int U = FEW ? 4 : UW, XS = FEW ? U : UX, XL = FEW ? 1 : 4 * MB;   // X: slots, loads per chunk
+            static_assert(!FEW || (MB == 1 && U * 512 <= UX * 2048), "the ring holds a row of each quarter");
+            u32x4 w[U][NB];
             auto load_w = [&](u32x4 (&d)[NB], int chunk) {
                 const uint8_t* wk = W + static_cast<int64_t>(chunk) * 64;
 #pragma unroll
@@ -276,18 +296,21 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
                     d[j] = *reinterpret_cast<const u32x4*>(wk + woff[j]);
             };
             // The wave's whole chunks of the panel from group p0 on: c0 + wave,
-            // c0 + wave + NWV, ... (`mine` of them); W of the first ones is on its
-            // way before anything else is computed.
+            // c0 + wave + NWV, ... (`mine` of them).
             int c0, mine;
             auto at = [&](int i) { return wave + (i < mine ? i : mine - 1) * NWV; };
-            auto start = [&](int p0) {
+            auto chunks = [&](int p0) {
                 c0 = p0 / NG;
                 mine = ((full < c0 + kPanel / NG ? full : c0 + kPanel / NG) - c0 - wave + NWV - 1) / NWV;
-                if (mine > 0)
-#pragma unroll
-                    for (int u = 0; u < UW - 1; ++u) load_w(w[u], c0 + at(u));
             };
-            start(0);
+            // W of the first chunks is on its way before anything else is computed
+            auto start = [&] {
+                if (!FEW && mine > 0)
+#pragma unroll
+                    for (int u = 0; u < U - 1; ++u) load_w(w[u], c0 + at(u));
+            };
+            chunks(0);
+            start();
             // Row i of a block of 16 sits in instruction row 4 (i % 4) + i / 4, so
             // that register r of the result holds rows 4 r .. 4 r + 3: blocks of up
             // to 4 rows scale one register in place of four.
@@ -296,17 +319,24 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
             // straight into the operand's lanes, consecutive lanes lie in different
             // rows, and the 16-row product took 32 us in place of 27).  Piece p of
             // row r sits at p ^ r.
-            const uint16_t* xsrc[MB][4];
+            const uint16_t* xsrc[FEW ? 1 : MB][FEW ? 1 : 4];
 #pragma unroll
-            for (int b = 0; b < MB; ++b)
+            for (int b = 0; b < (FEW ? 1 : MB); ++b)
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const int ir = 4 * t + g, i = m0 + 16 * b + t + 4 * g;
+                for (int t = 0; t < (FEW ? 1 : 4); ++t) {
+                    const int i = m0 + (FEW ? g : 16 * b + t + 4 * g);
                     xsrc[b][t] = a.X + static_cast<uint64_t>(static_cast<uint32_t>(row_of(i < rows ? i : rows - 1))) *
                                            static_cast<uint32_t>(a.sx) +
-                                 8 * ((lane & 15) ^ ir);
+                                 8 * ((lane & 15) ^ (FEW ? few_place<G>(g) : 4 * t + g));
                 }
-            const bool few = rows - m0 <= 4;
+            const bool few = FEW || ((MB > 1 || NB == 4) && rows - m0 <= 4);
+            uint32_t xaddr[4];   // this lane's pieces of X: instruction row lane % 16, FEW: row lane / 4 % 4
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int piece = (quarter_k<G>(g) + step_k<G>(t)) / 8, ir = lane & 15;
+                xaddr[t] = lds_addr(xwave) + (FEW ? (ir >> 2) * 256 + (piece ^ few_place<G>(ir >> 2)) * 16
+                                                  : ir * 256 + (piece ^ ir) * 16);
+            }
 
             f32x4 tot[MB][NB];
 #pragma unroll
@@ -315,6 +345,11 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
                 for (int j = 0; j < NB; ++j) tot[b][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
             auto load_x = [&](int slot, int chunk) {
+                if constexpr (FEW)
+                    __builtin_amdgcn_global_load_lds(
+                        (const __attribute__((address_space(1))) void*)(xsrc[0][0] + static_cast<int64_t>(chunk) * 128),
+                        (lds_void_t*)(xwave + slot * 512), 16, 0, 0);
+                else
 #pragma unroll
                 for (int b = 0; b < MB; ++b)
 #pragma unroll
@@ -328,20 +363,21 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
             // until every load in flight to LDS has landed.
             struct Frag {
                 u32x4 x[MB][4];
-                u32x2 q[NG][NB];
+                Scale q[NG][NB];
             };
             auto fetch = [&](auto slot_tag, Frag& f, int g0) {
                 static_for<4>([&](auto t_tag) {
                     static_for<MB>([&](auto b_tag) {
                         constexpr int T = decltype(t_tag)::value, B = decltype(b_tag)::value;
-                        f.x[B][T] = lds_read16<(decltype(slot_tag)::value * MB + B) * 4096>(xaddr[T]);
+                        f.x[B][T] = lds_read16<FEW ? decltype(slot_tag)::value * 1024 : (decltype(slot_tag)::value * MB + B) * 4096>(xaddr[T]);
                     });
                 });
-                const uint32_t taddr = tab_addr + 8 * g0;
+                const uint32_t taddr = tab_addr + sizeof(Entry) * g0;
                 static_for<NG>([&](auto i_tag) {
                     static_for<NB>([&](auto j_tag) {
                         constexpr int I = decltype(i_tag)::value, J = decltype(j_tag)::value;
-                        f.q[I][J] = lds_read8<(16 * J * kPitch + I) * 8>(taddr);
+                        if constexpr (ZP) f.q[I][J] = lds_read8<(16 * J * kPitch + I) * 8>(taddr);
+                        else f.q[I][J] = lds_read4<(16 * J * kPitch + I) * 4>(taddr);
                     });
                 });
             };
@@ -403,8 +439,11 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
                             for (int b = 0; b < MB; ++b)
 #pragma unroll
                                 for (int j = 0; j < NB; ++j)
-                                    tot[b][j][r] += __uint_as_float(f.q[I][j][0]) *
-                                                    (acc[b][j][r] - __uint_as_float(f.q[I][j][1]) * sum[b][r]);
+                                    if constexpr (ZP)
+                                        tot[b][j][r] += __uint_as_float(f.q[I][j][0]) *
+                                                        (acc[b][j][r] - __uint_as_float(f.q[I][j][1]) * sum[b][r]);
+                                    else
+                                        tot[b][j][r] += __uint_as_float(f.q[I][j]) * (acc[b][j][r] - 24.0f * sum[b][r]);
                         };
                         scale(0);
                         if (!few) {
@@ -418,12 +457,22 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
 
             for (int p0 = 0; p0 < groups; p0 += kPanel) {
                 const int held = groups - p0 < kPanel ? groups - p0 : kPanel;
-                if (mine > 0) {
-                    load_x(0, c0 + at(0));
-                    load_x(1, c0 + at(1));
+                const bool fresh = in_table != p0;
+                if constexpr (FEW) {   // in the order in which they are waited for
+                    if (fresh) load_table(p0, held);
+                    if (mine > 0) {
+                        static_for<U>([&](auto u_tag) { load_x(decltype(u_tag)::value, c0 + at(decltype(u_tag)::value)); });
+#pragma unroll
+                        for (int u = 0; u < U; ++u) load_w(w[u], c0 + at(u));
+                    }
+                } else {
+                    if (mine > 0) {
+                        load_x(0, c0 + at(0));
+                        load_x(1, c0 + at(1));
+                    }
+                    if (fresh) load_table(p0, held);
                 }
-                if (in_table != p0) {
-                    load_table(p0, held);
+                if (fresh) {
                     if (in_table >= 0) __syncthreads();   // the last panel's readers are done
                     store_table(held);
                     in_table = p0;
@@ -432,34 +481,45 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
                 // Step i contracts chunk i while the next one's operands come out of
                 // LDS, then refills their slot of the ring and W's registers.  X goes
                 // out before W: waiting for the next X leaves a later step of X and two
-                // of W in flight.
+                // of W in flight.  FEW: the first step's W is followed by U - 1 chunks of
+                // W and one of X, the later ones' by more.
                 Frag f[2];
                 auto step = [&](auto u_tag, int i) {
-                    constexpr int V = decltype(u_tag)::value, S1 = (V + 1) % UX;
-                    wait_vm<2 * NB + 4 * MB>();
-                    fetch(std::integral_constant<int, S1>{}, f[S1], at(i + 1) * NG);
-                    contract(f[V % UX], w[V]);
-                    landed(f[S1]);
-                    load_x(S1, c0 + at(i + 3));
-                    load_w(w[V], c0 + at(i + UW));
+                    constexpr int V = decltype(u_tag)::value, S1 = (V + 1) % XS, F1 = (V + 1) % 2;
+                    wait_vm<FEW ? NB * (U - 1) + 1 : 2 * NB + XL>();
+                    fetch(std::integral_constant<int, S1>{}, f[F1], at(i + 1) * NG);
+                    contract(f[V % 2], w[V]);
+                    landed(f[F1]);
+                    load_x(S1, c0 + at(i + 1 + XS));
+                    load_w(w[V], c0 + at(i + U));
                 };
                 if (mine > 0) {
                     // both chunks of X: fewer loads follow the second one here than the count in step() allows for
-                    wait_vm<0>();
+                    wait_vm<FEW ? NB * U + U - 1 : 0>();
                     fetch(std::integral_constant<int, 0>{}, f[0], at(0) * NG);
                     landed(f[0]);
-                    load_x(0, c0 + at(2));
-                    load_w(w[UW - 1], c0 + at(UW - 1));
-                    for (int i = 0;; i += UW) {
+                    load_x(0, c0 + at(XS));
+                    if constexpr (!FEW) load_w(w[U - 1], c0 + at(U - 1));
+                    for (int i = 0;; i += U) {
                         step(std::integral_constant<int, 0>{}, i);
                         if (i + 1 >= mine) break;
                         step(std::integral_constant<int, 1>{}, i + 1);
                         if (i + 2 >= mine) break;
-                        if constexpr (UW == 4) {
+                        if constexpr (U >= 4) {
                             step(std::integral_constant<int, 2>{}, i + 2);
                             if (i + 3 >= mine) break;
                             step(std::integral_constant<int, 3>{}, i + 3);
                             if (i + 4 >= mine) break;
+                        }
+                        if constexpr (U == 8) {
+                            step(std::integral_constant<int, 4>{}, i + 4);
+                            if (i + 5 >= mine) break;
+                            step(std::integral_constant<int, 5>{}, i + 5);
+                            if (i + 6 >= mine) break;
+                            step(std::integral_constant<int, 6>{}, i + 6);
+                            if (i + 7 >= mine) break;
+                            step(std::integral_constant<int, 7>{}, i + 7);
+                            if (i + 8 >= mine) break;
                         }
                     }
                     wait_vm<0>();   // no load may still be writing the ring
@@ -472,11 +532,11 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
 #pragma unroll
                     for (int j = 0; j < NB; ++j) w[0][j] = *reinterpret_cast<const u32x4*>(wk + (woff[j] - back));
 #pragma unroll
-                    for (int b = 0; b < MB; ++b)
+                    for (int b = 0; b < (FEW ? 1 : MB); ++b)
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) {
+                        for (int t = 0; t < (FEW ? 1 : 4); ++t) {
                             u32x4 v = {0, 0, 0, 0};
-                            if (k0 + 8 * ((lane & 15) ^ (4 * t + g)) < K)
+                            if (k0 + 8 * ((lane & 15) ^ (FEW ? few_place<G>(g) : 4 * t + g)) < K)
                                 v = *reinterpret_cast<const u32x4*>(xsrc[b][t] + k0);
                             *reinterpret_cast<u32x4*>(xwave + b * 2048 + t * 512 + 8 * lane) = v;
                         }
@@ -485,7 +545,10 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
                     landed(f[0]);
                     contract(f[0], w[0]);
                 }
-                if (p0 + kPanel < groups) start(p0 + kPanel);
+                if (p0 + kPanel < groups) {
+                    chunks(p0 + kPanel);
+                    start();
+                }
             }
 
             // ---- the waves' sums in wave order, rounded once (over the ring)
@@ -512,6 +575,15 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
                 a.Y[r * a.sy + n0 + n] = narrow<BF16>(v);
             }
             __syncthreads();   // red is written again by the next block of rows
+        };
+        for (int m0 = 0; m0 < rows; m0 += ROWS) {
+            if constexpr (MB == 1 && NB < 4) {
+                if (rows - m0 <= 4) {
+                    block(std::true_type{}, m0);
+                    continue;
+                }
+            }
+            block(std::false_type{}, m0);
         }
     }
 }
