@@ -105,6 +105,8 @@ gemm_status plan_impl(const gemm_w4_problem* prob, const gemm_device_info* dev, 
     //  four blocks, eight waves, where they still reach four CUs in five (16 x
     //    8192 x 14336: 22 us, two blocks 25; 8 x 8192 x 8192, 128 workgroups: 18
     //    us, two blocks 14);
+    //  two blocks, eight waves, where one workgroup to a CU is all there is and K
+    //    is short (16 x 608 x 7000: 7.3 us with four, 6.0; 16 x 2048: 6.7 and 7.6);
     //  else two blocks, four waves, two workgroups to a CU.
     int64_t used = matrices(prob);
     if (used > prob->M) used = prob->M > 0 ? prob->M : 1;
@@ -123,6 +125,8 @@ gemm_status plan_impl(const gemm_w4_problem* prob, const gemm_device_info* dev, 
             waves = 2;
         } else if (prob->group > 32 && 5 * used * cdiv(prob->N, 64) >= 4 * cus) {
             nb = 4;
+            waves = 8;
+        } else if (pairs <= cus && prob->K < 2048) {
             waves = 8;
         }
     }

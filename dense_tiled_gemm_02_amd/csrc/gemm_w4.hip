@@ -614,7 +614,7 @@ hipError_t launch_w4(const W4Args& a, int64_t tiles, hipStream_t stream) {
 
 const W4Entry kTable[] = {
     W4_GROUPS(1, 1, 8, 128), W4_GROUPS(2, 1, 4, 128), W4_WIDE(4, 1, 8, 128),
-    W4_GROUPS(1, 2, 4, 128), W4_GROUPS(2, 2, 4, 128), W4_GROUPS(2, 2, 2, 64), W4_GROUPS(2, 1, 1, 32), W4_GROUPS(2, 1, 2, 64),
+    W4_GROUPS(1, 2, 4, 128), W4_GROUPS(2, 2, 4, 128), W4_GROUPS(2, 2, 2, 64), W4_GROUPS(2, 1, 1, 32), W4_GROUPS(2, 1, 2, 64), W4_GROUPS(2, 1, 8, 128),
 };
 
 }  // namespace

@@ -61,3 +61,10 @@ def test_few_rows(M, N, K, G):
 @pytest.mark.parametrize("N,K,E", [(64, 1024, 8), (2000, 4096, 16), (700, 8192, 60), (36, 160, 64)])
 def test_few_rows_of_each_expert(N, K, E, G):
     run(30, N, K, G, torch.bfloat16, E, [(7 * m * m + m) % (E + 1) for m in range(30)])
+
+
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("M", [1, 7, 16])
+@pytest.mark.parametrize("N,K", [(4100, 32), (5000, 608), (7001, 1152), (8192, 2016)])
+def test_one_workgroup_to_a_cu_and_short_k(N, K, M, G):
+    run(M, N, K, G, torch.float16 if N % 2 else torch.bfloat16)
