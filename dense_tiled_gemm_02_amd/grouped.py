@@ -9,7 +9,7 @@ so nothing here synchronizes and every call can be captured in a graph.
     dX = grouped_matmul(dD, W.transpose(1, 2), offsets)
     dW = grouped_wgrad(X[order], dD, offsets)
 
-`grouped_linear` is grouped_matmul with these gradients, for autograd.
+`grouped_linear` is grouped_matmul with these gradients, for autograd (of any order).
 Argument marshalling only: the work runs in libgemm.so's HIP kernels.
 """
 import contextlib
@@ -311,6 +311,12 @@ def group_rows(ids, groups, stream=None):
     return _on_stream(call, ids.device, stream, (ids,))
 
 
+# Each one's gradients are made of the other, so they have derivatives of any
+# order.  A backward pass that no one differentiates calls the operators directly.
+def _differentiable():
+    return (grouped_linear, _GroupedWgrad.apply) if torch.is_grad_enabled() else (grouped_matmul, grouped_wgrad)
+
+
 class _GroupedLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, offsets):
@@ -320,13 +326,30 @@ class _GroupedLinear(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad):
         x, weight, offsets = ctx.saved_tensors
+        matmul, wgrad = _differentiable()
         grad = grad.contiguous()   # an expanded gradient (of a sum) would take the element-wise tiles
-        dx = grouped_matmul(grad, weight.transpose(1, 2), offsets) if ctx.needs_input_grad[0] else None
-        dw = grouped_wgrad(x, grad, offsets) if ctx.needs_input_grad[1] else None
+        dx = matmul(grad, weight.transpose(1, 2), offsets) if ctx.needs_input_grad[0] else None
+        dw = wgrad(x, grad, offsets) if ctx.needs_input_grad[1] else None
         return dx, dw, None
 
 
+class _GroupedWgrad(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, grad, offsets):
+        ctx.save_for_backward(x, grad, offsets)
+        return grouped_wgrad(x, grad, offsets)
+
+    @staticmethod
+    def backward(ctx, d):
+        x, grad, offsets = ctx.saved_tensors
+        matmul, _ = _differentiable()
+        d = d.contiguous()
+        dx = matmul(grad, d.transpose(1, 2), offsets) if ctx.needs_input_grad[0] else None
+        dgrad = matmul(x, d, offsets) if ctx.needs_input_grad[1] else None
+        return dx, dgrad, None
+
+
 def grouped_linear(x, weight, offsets):
-    """grouped_matmul(x, weight, offsets) with gradients for x (R x K) and
-    weight (E x K x N)."""
+    """grouped_matmul(x, weight, offsets) with gradients, of any order, for x
+    (R x K) and weight (E x K x N)."""
     return _GroupedLinear.apply(x, weight, offsets)
