@@ -104,6 +104,8 @@ def w4_matvec(X, W, scale, zeros=None, group=128, experts=None, out=None, stream
 
     def call():
         Y = out if out is not None else torch.empty((M, N), dtype=X.dtype, device=X.device)
+        if experts is not None and W.shape[0] == 0:   # no matrix: every row is outside
+            return Y.zero_()
         key = (X.device.index, X.dtype, M, X.stride(0), W.shape, W.stride(), scale.stride(),
                None if zeros is None else zeros.stride(), group, None if experts is None else experts.dtype,
                Y.stride(0))
@@ -132,8 +134,6 @@ def w4_matvec(X, W, scale, zeros=None, group=128, experts=None, out=None, stream
         if plain:
             _remember(W4, plan, "gemm_w4_run", 0, (M, N), X.dtype, group, X, W, scale, zeros, experts)
         return Y
-    if experts is not None and W.shape[0] == 0:   # no matrix: every row is outside
-        return out.zero_() if out is not None else torch.zeros((M, N), dtype=X.dtype, device=X.device)
     return _on_stream(call, X.device, stream, (X, W, scale, zeros, experts, out))
 
 
