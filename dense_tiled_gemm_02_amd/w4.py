@@ -113,12 +113,12 @@ def w4_matvec(X, W, scale, zeros=None, group=128, experts=None, out=None, stream
         if plan is None:
             p = gemm_w4_problem()
             p.M, p.N, p.K, p.group = M, N, K, group
-            p.sx = X.stride(0) if M > 1 else 0
+            p.sx = X.stride(0) if M > 1 and K > 0 else 0   # strides that no access uses are not looked at
             p.sy = Y.stride(0)
-            p.sw_n, p.ss_n = W.stride(-2) if N > 1 else 0, scale.stride(-2)
+            p.sw_n, p.ss_n = W.stride(-2) if N > 1 and K > 0 else 0, scale.stride(-2)
             if experts is not None:
                 p.experts, p.id_bytes = W.shape[0], experts.element_size()
-                p.sw_e, p.ss_e = W.stride(0) if W.shape[0] > 1 else 0, scale.stride(0)
+                p.sw_e, p.ss_e = W.stride(0) if W.shape[0] > 1 and K > 0 else 0, scale.stride(0)
             if zeros is not None:
                 p.has_zeros, p.sz_n = 1, zeros.stride(-2)
                 p.sz_e = zeros.stride(0) if experts is not None else 0
