@@ -320,6 +320,18 @@ def gemm_streamk_pieces(tiles, k_steps, workgroups, wg):
 
 # ---------------------------------------------------------------- torch convenience
 
+_MOST_PLANS = 4096   # of each cache: where row counts vary, every one is a plan
+
+
+def _keep_plan(plans, key, plan):
+    """plans[key] = plan, all others dropped first where the cache is full.  A
+    plan lives as long as a call holds it."""
+    if len(plans) >= _MOST_PLANS:
+        plans.clear()
+    plans[key] = plan
+    return plan
+
+
 def problem(M, N, K, dtype, has_c=False, lda=None, ldb=None, ldc=None, ldd=None, ta=False, tb=False):
     """A gemm_problem with row-major C, D and, unless ta / tb, row-major A, B.
     ta: A stored K x M (element (m, k) at m + k * lda); tb: B stored N x K

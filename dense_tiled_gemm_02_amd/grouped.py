@@ -19,7 +19,8 @@ import threading
 import torch
 
 from . import (GEMM_BF16, GEMM_F16, GEMM_GROUPED_OUT_F32, GEMM_GROUPED_OUT_SAME, GEMM_GROUPED_REDUCE,
-               GEMM_GROUPED_ROWS, _check, _force, _i32, _i64, _p, binding, gemm_config, gemm_grouped_problem, lib)
+               GEMM_GROUPED_ROWS, _check, _force, _i32, _i64, _keep_plan, _p, binding, gemm_config,
+               gemm_grouped_problem, lib)
 
 _CODES = {torch.float16: GEMM_F16, torch.bfloat16: GEMM_BF16}
 
@@ -200,7 +201,7 @@ def _run(kind, A, B, offsets, out, groups, P, Q, accumulate, config):
         with _lock:
             plan = _plans.get(key)
             if plan is None:
-                plan = _plans[key] = gemm_grouped_plan_create(p, A.device.index, config)
+                plan = _keep_plan(_plans, key, gemm_grouped_plan_create(p, A.device.index, config))
     _launch(plan, A, B, offsets, out, _raw_stream(A.device.index))
     return plan
 

@@ -9,7 +9,7 @@ nibble); SA / SB hold one E8M0 scale byte per 32 k of each row.
 import ctypes
 import threading
 
-from . import (GemmError, _check, _force, _i32, _i64, _p, gemm_config, gemm_device_info, gemm_last_error,
+from . import (GemmError, _check, _force, _i32, _i64, _keep_plan, _p, gemm_config, gemm_device_info, gemm_last_error,
                lib)
 
 GEMM_MX_E4M3 = 0
@@ -202,7 +202,7 @@ def mx_matmul(A, SA, B, SB, K, fmt_a="e4m3", fmt_b=None, C=None, out=None, out_d
     with _cache_lock:
         pl = _plans.get(key)
         if pl is None:
-            pl = _plans[key] = gemm_mx_plan_create(p, dev, config)
+            pl = _keep_plan(_plans, key, gemm_mx_plan_create(p, dev, config))
     if stream is None:
         stream = torch.cuda.current_stream(A.device).cuda_stream
     elif hasattr(stream, "cuda_stream"):

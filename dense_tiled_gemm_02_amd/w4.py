@@ -11,7 +11,7 @@ import threading
 
 import torch
 
-from . import GEMM_BF16, GEMM_F16, _check, _p, gemm_w4_problem, lib
+from . import GEMM_BF16, GEMM_F16, _check, _keep_plan, _p, gemm_w4_problem, lib
 from .grouped import W4, _need_gpu, _on_stream, _raw_stream, _remember, _remembered
 
 _CODES = {torch.float16: GEMM_F16, torch.bfloat16: GEMM_BF16}
@@ -126,7 +126,7 @@ def w4_matvec(X, W, scale, zeros=None, group=128, experts=None, out=None, stream
             with _lock:
                 plan = _plans.get(key)
                 if plan is None:
-                    plan = _plans[key] = gemm_w4_plan_create(p, X.device.index)
+                    plan = _keep_plan(_plans, key, gemm_w4_plan_create(p, X.device.index))
         gemm_w4_run(plan, X.data_ptr(), W.data_ptr(), scale.data_ptr(),
                     zeros.data_ptr() if zeros is not None else None,
                     experts.data_ptr() if experts is not None else None, Y.data_ptr(),
