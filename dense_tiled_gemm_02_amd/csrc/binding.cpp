@@ -14,7 +14,8 @@
 //   forget()
 //
 // Only plain torch.Tensor and Parameter objects on a GPU are looked up.  The
-// interpreter's lock guards the table.
+// interpreter's lock guards the table; it is released for the allocations and
+// the launch, which waits while the GPU's queue is full.
 #include <Python.h>
 #include <ATen/ATen.h>
 #include <c10/hip/HIPFunctions.h>
@@ -24,7 +25,6 @@
 #include <cstring>
 #include <unordered_map>
 #include <utility>
-#include <vector>
 
 namespace {
 
@@ -61,7 +61,8 @@ struct Entry {
     void* run;
     void* plan;
     int64_t workspace;
-    std::vector<int64_t> sizes;   // of the output; rows: {groups, R, id bytes}
+    int64_t sizes[3];   // of the output, `dims` of them; rows: {groups, R, id bytes}
+    int dims;
     at::ScalarType dtype;
 };
 
@@ -113,40 +114,51 @@ at::Tensor make(at::IntArrayRef sizes, at::ScalarType dtype, const at::Tensor& l
     return at::empty(sizes, at::TensorOptions().dtype(dtype).device(like.device()));
 }
 
-PyObject* status_of(int st) { return PyLong_FromLong(st); }
+struct Unlocked {   // the interpreter's lock, released
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
 
-PyObject* launch(int kind, const Entry& e, PyObject* const* t) {
-    const at::Tensor& first = THPVariable_Unpack(t[0]);
+struct Held {   // a reference
+    PyObject* o;
+    explicit Held(PyObject* owner) : o(owner) { Py_INCREF(o); }
+    ~Held() { Py_DECREF(o); }
+};
+
+// The outputs of one launch (`order`: of the rows) and its status.
+struct Result {
+    at::Tensor out, order;
+    int status;
+};
+
+Result launch(int kind, const Entry& e, const at::Tensor& like, const void* const* in) {
+    Result r;
+    at::Tensor ws;   // released on return: later work of this stream may reuse it, in order
     void* const stream = c10::hip::getCurrentHIPStream(static_cast<c10::DeviceIndex>(e.device)).stream();
     if (kind == kRows) {
         typedef int (*fn)(const void*, int32_t, int64_t, int64_t, void*, void*, void*, size_t, void*);
-        at::Tensor offsets = make({e.sizes[0] + 1}, at::kInt, first), order = make({e.sizes[1]}, at::kInt, first), ws;
-        if (e.workspace > 0) ws = make({e.workspace}, at::kByte, first);
-        const int st = reinterpret_cast<fn>(e.run)(data(t[0]), static_cast<int32_t>(e.sizes[2]), e.sizes[1], e.sizes[0],
-                                                   offsets.data_ptr(), order.data_ptr(),
-                                                   e.workspace > 0 ? ws.data_ptr() : nullptr, e.workspace, stream);
-        if (st != 0) return status_of(st);
-        PyObject* pair = PyTuple_New(2);
-        PyTuple_SET_ITEM(pair, 0, THPVariable_Wrap(std::move(offsets)));
-        PyTuple_SET_ITEM(pair, 1, THPVariable_Wrap(std::move(order)));
-        return pair;
+        r.out = make({e.sizes[0] + 1}, at::kInt, like);
+        r.order = make({e.sizes[1]}, at::kInt, like);
+        if (e.workspace > 0) ws = make({e.workspace}, at::kByte, like);
+        r.status = reinterpret_cast<fn>(e.run)(in[0], static_cast<int32_t>(e.sizes[2]), e.sizes[1], e.sizes[0],
+                                               r.out.data_ptr(), r.order.data_ptr(),
+                                               e.workspace > 0 ? ws.data_ptr() : nullptr, e.workspace, stream);
+        return r;
     }
-    at::Tensor out = make(e.sizes, e.dtype, first);
-    int st;
+    r.out = make(at::IntArrayRef(e.sizes, e.dims), e.dtype, like);
     if (kind == kW4) {
         typedef int (*fn)(void*, const void*, const void*, const void*, const void*, const void*, void*, void*);
-        st = reinterpret_cast<fn>(e.run)(e.plan, data(t[0]), data(t[1]), data(t[2]), data(t[3]), data(t[4]),
-                                         out.data_ptr(), stream);
+        r.status = reinterpret_cast<fn>(e.run)(e.plan, in[0], in[1], in[2], in[3], in[4], r.out.data_ptr(), stream);
     } else {
         typedef int (*fn)(void*, const void*, const void*, const void*, void*, void*, size_t, void*);
-        at::Tensor ws;   // released on return: later work of this stream may reuse it, in order
-        if (e.workspace > 0) ws = make({e.workspace}, at::kByte, first);
-        st = reinterpret_cast<fn>(e.run)(e.plan, data(t[0]), data(t[1]), data(t[2]), out.data_ptr(),
-                                         e.workspace > 0 ? ws.data_ptr() : nullptr, e.workspace, stream);
+        if (e.workspace > 0) ws = make({e.workspace}, at::kByte, like);
+        r.status = reinterpret_cast<fn>(e.run)(e.plan, in[0], in[1], in[2], r.out.data_ptr(),
+                                               e.workspace > 0 ? ws.data_ptr() : nullptr, e.workspace, stream);
     }
-    return st != 0 ? status_of(st) : THPVariable_Wrap(std::move(out));
+    return r;
 }
 
+constexpr int kMostOperands = 5;
 int operands(int kind) { return kind == kRows ? 1 : kind == kW4 ? 5 : 3; }
 
 bool read_key(Key* key, PyObject* extra, PyObject* const* t, int n, int* device) {
@@ -170,7 +182,22 @@ PyObject* py_call(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const auto& calls = table(kind);
         const auto hit = calls.find(key);
         if (hit == calls.end() || c10::hip::current_device() != hit->second.device) Py_RETURN_NONE;
-        return launch(static_cast<int>(kind), hit->second, args + 2);
+        const Entry e = hit->second;   // the table may change while the lock is released
+        const Held plan(e.owner);
+        const at::Tensor like = THPVariable_Unpack(args[2]);
+        const void* in[kMostOperands];
+        for (int i = 0; i < operands(kind); ++i) in[i] = data(args[2 + i]);
+        Result r;
+        {
+            const Unlocked unlocked;
+            r = launch(static_cast<int>(kind), e, like, in);
+        }
+        if (r.status != 0) return PyLong_FromLong(r.status);
+        if (kind != kRows) return THPVariable_Wrap(std::move(r.out));
+        PyObject* pair = PyTuple_New(2);
+        PyTuple_SET_ITEM(pair, 0, THPVariable_Wrap(std::move(r.out)));
+        PyTuple_SET_ITEM(pair, 1, THPVariable_Wrap(std::move(r.order)));
+        return pair;
     } catch (const std::exception& ex) {
         PyErr_SetString(PyExc_RuntimeError, ex.what());
         return nullptr;
@@ -185,22 +212,24 @@ PyObject* py_remember(PyObject*, PyObject* args) {
     if (!PyArg_ParseTuple(args, "iOKKLO!OOO!", &kind, &owner, &plan, &run, &workspace, &PyTuple_Type, &sizes, &dtype, &extra,
                           &PyTuple_Type, &tensors))
         return nullptr;
-    if (kind < 0 || kind >= kKinds || PyTuple_GET_SIZE(tensors) != operands(kind) || !THPDtype_Check(dtype)) {
-        PyErr_SetString(PyExc_TypeError, "remember: kind, dtype or tensors do not fit");
+    if (kind < 0 || kind >= kKinds || PyTuple_GET_SIZE(tensors) != operands(kind) || !THPDtype_Check(dtype) ||
+        PyTuple_GET_SIZE(sizes) > 3) {
+        PyErr_SetString(PyExc_TypeError, "remember: kind, sizes, dtype or tensors do not fit");
         return nullptr;
     }
     try {
         Key key;
         Entry e;
-        PyObject* t[5];
+        PyObject* t[kMostOperands];
         for (int i = 0; i < operands(kind); ++i) t[i] = PyTuple_GET_ITEM(tensors, i);
         if (!read_key(&key, extra, t, operands(kind), &e.device) || e.device < 0) Py_RETURN_NONE;
         e.plan = reinterpret_cast<void*>(static_cast<uintptr_t>(plan));
         e.run = reinterpret_cast<void*>(static_cast<uintptr_t>(run));
         e.workspace = workspace;
         e.dtype = reinterpret_cast<THPDtype*>(dtype)->scalar_type;
-        for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(sizes); ++i) {
-            e.sizes.push_back(PyLong_AsLongLong(PyTuple_GET_ITEM(sizes, i)));
+        e.dims = static_cast<int>(PyTuple_GET_SIZE(sizes));
+        for (int i = 0; i < e.dims; ++i) {
+            e.sizes[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(sizes, i));
             if (PyErr_Occurred()) return nullptr;
         }
         auto& calls = table(kind);
