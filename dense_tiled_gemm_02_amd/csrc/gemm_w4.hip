@@ -72,6 +72,11 @@ __device__ __forceinline__ uint32_t offset_pair(uint32_t w, uint32_t mask, uint3
     return (v & mask) | sixteen;
 }
 
+// Between X's loads and W's.  A wait for X counts the loads that follow it, so
+// X has to go out first; nothing else keeps the scheduler from moving W's.  Only
+// memory loads are held (mask: arithmetic, matrix and LDS instructions may pass).
+__device__ __forceinline__ void x_before_w() { __builtin_amdgcn_sched_barrier(0x48F); }
+
 // X's 8 consecutive k in the nibbles' pair order: (k, k + 4) for k = 0..3.
 __device__ __forceinline__ u32x4 pair_order(u32x4 x) {
     return u32x4{__builtin_amdgcn_perm(x[2], x[0], 0x05040100), __builtin_amdgcn_perm(x[2], x[0], 0x07060302),
@@ -462,6 +467,7 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
                     if (fresh) load_table(p0, held);
                     if (mine > 0) {
                         static_for<U>([&](auto u_tag) { load_x(decltype(u_tag)::value, c0 + at(decltype(u_tag)::value)); });
+                        x_before_w();
 #pragma unroll
                         for (int u = 0; u < U; ++u) load_w(w[u], c0 + at(u));
                     }
@@ -491,6 +497,7 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
                     contract(f[V % 2], w[V]);
                     landed(f[F1]);
                     load_x(S1, c0 + at(i + 1 + XS));
+                    x_before_w();
                     load_w(w[V], c0 + at(i + U));
                 };
                 if (mine > 0) {
@@ -499,6 +506,7 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
                     fetch(std::integral_constant<int, 0>{}, f[0], at(0) * NG);
                     landed(f[0]);
                     load_x(0, c0 + at(XS));
+                    x_before_w();
                     if constexpr (!FEW) load_w(w[U - 1], c0 + at(U - 1));
                     for (int i = 0;; i += U) {
                         step(std::integral_constant<int, 0>{}, i);
