@@ -148,7 +148,7 @@ def w4_quantize(W, group=128, zeros=False):
         raise ValueError("K=%d must be a multiple of 32" % K)
     n = -(-K // group)
     w = torch.nn.functional.pad(W.float(), (0, n * group - K)).unflatten(-1, (n, group))
-    tiny = torch.finfo(W.dtype).tiny
+    tiny = torch.finfo(W.dtype).tiny * torch.finfo(W.dtype).eps   # the smallest scale above zero
     if zeros:
         lo, hi = w.amin(-1).clamp(max=0.0), w.amax(-1).clamp(min=0.0)
         scale = ((hi - lo) / 15).clamp(min=tiny).to(W.dtype)
