@@ -260,9 +260,9 @@ def grouped_wgrad(A, G, offsets, out=None, out_dtype=None, accumulate=False, con
     _operands(A, G, 2)
     if A.shape[0] != G.shape[0]:
         raise ValueError("row counts differ: %s and %s" % (tuple(A.shape), tuple(G.shape)))
+    if offsets.dim() != 1 or offsets.shape[0] == 0:
+        raise ValueError("offsets must hold at least one value in one dimension")
     E, K, N = offsets.shape[0] - 1, A.shape[1], G.shape[1]
-    if E < 0:
-        raise ValueError("offsets must hold at least one value")
     _need_gpu(A.device, ("A", A), ("G", G), ("offsets", offsets), ("out", out))
     _offsets_arg(offsets, E, A.device)
     if accumulate and out is None:

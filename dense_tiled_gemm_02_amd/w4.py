@@ -143,6 +143,10 @@ def w4_quantize(W, group=128, zeros=False):
     largest magnitude (zero is None), or, with zeros, against its range."""
     if W.dtype not in _CODES:
         raise TypeError("W must be float16 or bfloat16, got %s" % W.dtype)
+    if W.dim() == 0:
+        raise ValueError("W must have rows")
+    if group <= 0:
+        raise ValueError("group must be positive, got %d" % group)
     K = W.shape[-1]
     if K % 32:
         raise ValueError("K=%d must be a multiple of 32" % K)
