@@ -513,21 +513,11 @@ __global__ __launch_bounds__(64 * NWV, 2) void gemm_w4_kernel(W4Args a) {
                         if (i + 1 >= mine) break;
                         step(std::integral_constant<int, 1>{}, i + 1);
                         if (i + 2 >= mine) break;
-                        if constexpr (U >= 4) {
+                        if constexpr (U == 4) {
                             step(std::integral_constant<int, 2>{}, i + 2);
                             if (i + 3 >= mine) break;
                             step(std::integral_constant<int, 3>{}, i + 3);
                             if (i + 4 >= mine) break;
-                        }
-                        if constexpr (U == 8) {
-                            step(std::integral_constant<int, 4>{}, i + 4);
-                            if (i + 5 >= mine) break;
-                            step(std::integral_constant<int, 5>{}, i + 5);
-                            if (i + 6 >= mine) break;
-                            step(std::integral_constant<int, 6>{}, i + 6);
-                            if (i + 7 >= mine) break;
-                            step(std::integral_constant<int, 7>{}, i + 7);
-                            if (i + 8 >= mine) break;
                         }
                     }
                     wait_vm<0>();   // no load may still be writing the ring
