@@ -1,7 +1,8 @@
 // Native side of the torch calls that grouped.py and w4.py have already checked
 // once: from the arguments' types, shapes, strides and devices to the plan and
 // the launch, without Python in between.  A decode-sized product is bound by
-// its host time, 6.7 us through ctypes and 4.6 us here, 3 of them the launch.
+// its host time: 4.1 to 4.9 us here, 3.4 of them the library's call, against 7.4
+// where the call is checked (out given) and passed on by ctypes.
 //
 //   remember(kind, owner, plan, run, workspace, sizes, dtype, extra, tensors)
 //       a call that passed the checks: its gemm_*_run address, plan handle (kept

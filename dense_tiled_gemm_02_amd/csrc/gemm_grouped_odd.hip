@@ -89,9 +89,10 @@ __device__ __forceinline__ void odd_tile(const KArgs& p, int pid_m, int pid_n) {
 #pragma unroll
     for (int i = 0; i < PB; ++i) lb[i] = place(std::integral_constant<bool, BKC>{}, OB{}, i, p.B, ldb, n0, p.N);
 
-    // Every lane loads at every step: without branches around them the compiler
-    // counts the loads in flight.  Past the whole steps, lanes with no k left
-    // read the operand's start.
+    // Every lane loads at every step, so that the compiler counts the loads in
+    // flight (the branches left are a whole wave's, around the last steps'
+    // addresses).  Past the whole steps, lanes with no k left read the operand's
+    // start.
     const int whole = K / BK;
     auto fetch = [&](auto kc_tag, Lane& l, const uint16_t* op, int kt) {
         const uint16_t* src = l.src;

@@ -23,7 +23,7 @@
 // The epilogue adds C in fp32 once, rounds to the storage type (nearest even)
 // and stores only rows < M and columns < N.
 //
-// (The tile body; gemm_tile.hip and gemm_grouped.hip hold the kernels that
+// (The tile body; gemm_tile.hip and gemm_grouped_any.hip hold the kernels that
 // choose a workgroup's tile.)
 #pragma once
 

@@ -20,9 +20,9 @@
 // infinite) is summed again term by term.
 //
 // A wave takes chunks of 128 k of 16 NB rows of W: each lane one 16-byte load
-// per 16 rows (row l mod 16, k 32 (l / 16) .. + 31), UW chunks ahead in
+// per 16 rows (row l mod 16, k 32 (l / 16) .. + 31), issued UW chunks ahead into
 // registers (cached: non-temporal, the two waves that share each 128-byte line
-// both fetch it, 24 us in place of 22 below); X comes through a ring in LDS,
+// both fetch it, 24 us in place of 22 when that was tried); X comes through a ring in LDS,
 // filled by direct loads; the scales and offsets of the workgroup's columns are
 // converted into an LDS table once.  The order of k inside the instruction is
 // free as long as X follows it, so with groups of 128 a lane's four dwords are
@@ -33,16 +33,21 @@
 // depend on timing.
 //
 // Blocks of up to 4 rows (a token, or the few rows of one of many experts) load
-// and keep a quarter of X, four chunks ahead like W: 1 x 4096 x 4096 6.1 -> 5.6
-// us, 32 rows over 16 experts, 4096 x 2048, groups of 32 24 -> 21 us (eight
-// chunks ahead: 22).
+// and keep a quarter of X, issued four chunks ahead like W: 1 x 4096 x 4096 6.1 ->
+// 5.6 us, 32 rows over 16 experts, 4096 x 2048, groups of 32 24 -> 21 us (eight
+// chunks ahead: 22) when they came in; 5.3 and 19 us now.  Four column blocks (one
+// row of 8192 x 14336, groups of 128: 16.9 us) have no such path.
 //
-// Measured: 16 x 8192 x 14336, groups of 64 with zero points, 20.5 us with W from
-// memory (18.2 us from the caches), against 13.0 us for reading W alone in this
-// order of lanes (10.5 us in consecutive 1 KB); 1 x 4096 x 4096 5.6 us.  Bound by
-// the loads that two waves per SIMD keep in flight (half of a wave's cycles
-// wait) and by 3 us before the first product; vector instructions, about 70 per
-// 1 KB of W, issue in a third of the cycles.  With many workgroups those 3 us
+// What is issued ahead does not stay in flight for a whole round of UW chunks:
+// as compiled, one wait in a round (two where UW is 2) is for every load there
+// is, the compiler's own for W's registers while loads to LDS are pending, and
+// the loop pays a memory latency there.
+//
+// Measured: 16 x 8192 x 14336, groups of 64 with zero points, 19.3 us with W from
+// memory, against 13.0 us for reading W alone in this order of lanes (10.5 us in
+// consecutive 1 KB).  Bound by those waits (half of a wave's cycles) and by 3 us
+// before the first product; vector instructions, about 70 per 1 KB of W, issue
+// in a third of the cycles.  With many workgroups those 3 us
 // count most, and one wave with 32 columns to itself wins (30 rows over 60
 // experts, 1024 x 2786: 20 us, 44 with four waves to 32 columns).
 #include <hip/hip_runtime.h>

@@ -103,7 +103,7 @@ _lock = threading.Lock()   # guards _plans
 # The plain calls (no out, config or stream) that passed every check are
 # remembered by _binding.so, by what the checks look at: the operands' types,
 # shapes, strides and devices.  A call found there goes straight to the launch:
-# 4.7 us of host time instead of 11, which is what the smallest products take.
+# 4.1 to 4.9 us of host time instead of 7.4, which is what the smallest products take.
 MATMUL, WGRAD, ROWS, W4 = range(4)   # csrc/binding.cpp
 _call = None
 _raw_stream = torch._C._cuda_getCurrentRawStream

@@ -303,7 +303,9 @@ gemm_status gemm_streamk_pieces(int32_t tiles, int32_t k_steps, int32_t workgrou
  * Any strides >= 0 of A and B run; the direct-to-LDS tiles take A and B with a
  * contiguous index (A along P; B along Q, or along P for GEMM_GROUPED_ROWS)
  * whose extent and whose other strides are multiples of 8, with 16-byte
- * aligned bases; everything else runs on an element-wise tile. */
+ * aligned bases.  Operands with such an index of 8 elements or more and any
+ * other sizes, strides or bases run on a tile with 16-byte loads at any
+ * address; the rest (broadcast or twice-strided views) element by element. */
 typedef enum gemm_grouped_kind { GEMM_GROUPED_ROWS = 0, GEMM_GROUPED_REDUCE = 1 } gemm_grouped_kind;
 
 typedef enum gemm_grouped_out {
