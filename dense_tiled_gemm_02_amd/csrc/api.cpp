@@ -79,6 +79,7 @@ gemm_status validate(const gemm_problem* p) {
         return fail(GEMM_ERR_INVALID_ARG, "has_c must be 0 or 1, got %d", (int)p->has_c);
     if (p->M > kMaxDim || p->N > kMaxDim || p->K > kMaxDim)
         return fail(GEMM_ERR_UNSUPPORTED, "dimensions above 2^31-1 are not supported");
+    if (p->K > dtg::kMaxSize) return fail(GEMM_ERR_UNSUPPORTED, "K above 2^31-4096 is not supported");
     const int64_t rs[4] = {p->sa_m, p->sb_k, p->sc_m, p->sd_m};
     const int64_t cs[4] = {p->sa_k, p->sb_n, p->sc_n, p->sd_n};
     const char* nm[4] = {"A", "B", "C", "D"};

@@ -82,8 +82,8 @@ gemm_status validate(const gemm_grouped_problem* p) {
         return fail(GEMM_ERR_INVALID_ARG, "accumulate must be 0 or 1, got %d", (int)p->accumulate);
     if (!reduce_kind(p) && (p->out != GEMM_GROUPED_OUT_SAME || p->accumulate))
         return fail(GEMM_ERR_UNSUPPORTED, "fp32 output and accumulate are of GEMM_GROUPED_REDUCE only");
-    if (p->R > kMaxDim || p->P > kMaxDim || p->Q > kMaxDim)
-        return fail(GEMM_ERR_UNSUPPORTED, "dimensions above 2^31-1 are not supported");
+    if (p->R > dtg::kMaxSize || p->P > dtg::kMaxSize || p->Q > dtg::kMaxSize)
+        return fail(GEMM_ERR_UNSUPPORTED, "dimensions above 2^31-4096 are not supported");
     if (p->groups > kMaxGroups)
         return fail(GEMM_ERR_UNSUPPORTED, "%lld groups, at most %lld", (long long)p->groups, (long long)kMaxGroups);
     if (p->sa_r < 0 || p->sa_p < 0 || p->sb_g < 0 || p->sb_r < 0 || p->sb_q < 0 || p->sd_g < 0 || p->sd_r < 0)

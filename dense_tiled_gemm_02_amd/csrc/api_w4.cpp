@@ -69,8 +69,8 @@ gemm_status validate(const gemm_w4_problem* p) {
         return fail(GEMM_ERR_INVALID_ARG, "id_bytes must be 4 or 8, got %d", (int)p->id_bytes);
     if (p->group != 32 && p->group != 64 && p->group != 128)
         return fail(GEMM_ERR_UNSUPPORTED, "group=%lld: scales are per 32, 64 or 128 k", (long long)p->group);
-    if (p->M > kMaxDim || p->N > kMaxDim || p->K > kMaxDim)
-        return fail(GEMM_ERR_UNSUPPORTED, "dimensions above 2^31-1 are not supported");
+    if (p->M > dtg::kMaxSize || p->N > dtg::kMaxSize || p->K > dtg::kMaxSize)
+        return fail(GEMM_ERR_UNSUPPORTED, "dimensions above 2^31-4096 are not supported");
     if (p->experts > 65535)
         return fail(GEMM_ERR_UNSUPPORTED, "%lld experts, at most 65535", (long long)p->experts);
     if (p->K % 32) return fail(GEMM_ERR_UNSUPPORTED, "K=%lld must be a multiple of 32", (long long)p->K);

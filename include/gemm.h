@@ -97,7 +97,7 @@ typedef enum gemm_status {
 
 /* The problem.  Strides are in elements.  sc_* are ignored when has_c == 0. */
 typedef struct gemm_problem {
-    int64_t M, N, K;
+    int64_t M, N, K;            /* below 2^31; K up to 2^31 - 4096 */
     int64_t sa_m, sa_k;         /* A: element (i, k) at A[i*sa_m + k*sa_k] */
     int64_t sb_k, sb_n;         /* B: element (k, j) at B[k*sb_k + j*sb_n] */
     int64_t sc_m, sc_n;         /* C: element (i, j) at C[i*sc_m + j*sc_n] */
@@ -313,7 +313,8 @@ typedef enum gemm_grouped_out {
     GEMM_GROUPED_OUT_F32 = 1    /* fp32 D (GEMM_GROUPED_REDUCE only) */
 } gemm_grouped_out;
 
-/* Strides in elements; D's column stride is 1.  At most 65535 groups. */
+/* Strides in elements; D's column stride is 1.  At most 65535 groups; R, P and Q
+ * up to 2^31 - 4096. */
 typedef struct gemm_grouped_problem {
     int64_t groups, R, P, Q;
     int64_t sa_r, sa_p;         /* A: element (i, p) at A[i*sa_r + p*sa_p] */
@@ -390,7 +391,7 @@ gemm_status gemm_group_rows_workspace(int64_t R, int64_t groups, size_t* bytes);
  * of the exact value (the sums run over q + 16 and are corrected: 31 bounds
  * that offset's part; with zero points above 15, 31 + z takes its place).  Bitwise reproducible for a fixed plan. */
 typedef struct gemm_w4_problem {
-    int64_t M, N, K, group;     /* K a multiple of 32 */
+    int64_t M, N, K, group;     /* K a multiple of 32; each up to 2^31 - 4096 */
     int64_t experts;            /* 0: one matrix for every row; at most 65535 */
     int64_t sx, sy;             /* row strides of X (multiple of 8, below 2^31) and Y, elements */
     int64_t sw_n, sw_e;         /* W: row (below 2^26) and expert strides, bytes, multiples of 16 */
