@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(_HERE, "libgemm.so")
 GEMM_F16 = 0
 GEMM_BF16 = 1
 GEMM_I8 = 2     # int8 A and B (k contiguous), int32 C and D
+GEMM_F32 = 3    # of the row operators and the scaled int8 product alone
 GEMM_OK = 0
 GEMM_ERR_INVALID_ARG = 1
 GEMM_ERR_UNSUPPORTED = 2
@@ -29,6 +30,8 @@ GEMM_GROUPED_ROWS = 0     # D (R x Q) = A (R x P) x B[group of the row] (P x Q)
 GEMM_GROUPED_REDUCE = 1   # D[group] (P x Q) = A_g^T x B_g over the group's rows
 GEMM_GROUPED_OUT_SAME = 0
 GEMM_GROUPED_OUT_F32 = 1
+GEMM_SCORE_SOFTMAX = 0
+GEMM_SCORE_SIGMOID = 1
 GEMM_STATIC_SCRATCH_BYTES = 24 << 20   # include/gemm.h: the workspace gemm_run_static provides
 KERNEL_TILE = 1
 KERNEL_SKINNY = 2
@@ -73,6 +76,17 @@ class gemm_w4_problem(ctypes.Structure):
                 ("sx", _i64), ("sy", _i64), ("sw_n", _i64), ("sw_e", _i64), ("ss_n", _i64), ("ss_e", _i64),
                 ("sz_n", _i64), ("sz_e", _i64),
                 ("dtype", ctypes.c_int), ("has_zeros", _i32), ("id_bytes", _i32)]
+
+
+class gemm_norm_problem(ctypes.Structure):
+    _fields_ = [("R", _i64), ("K", _i64), ("sx", _i64), ("sr", _i64), ("sh", _i64), ("sy", _i64),
+                ("dtype", ctypes.c_int), ("weight", ctypes.c_int), ("has_residual", _i32), ("eps", ctypes.c_float)]
+
+
+class gemm_route_problem(ctypes.Structure):
+    _fields_ = [("R", _i64), ("sl", _i64), ("E", _i32), ("top", _i32), ("groups", _i32), ("top_groups", _i32),
+                ("group_best", _i32), ("has_bias", _i32), ("renormalize", _i32), ("scale", ctypes.c_float),
+                ("dtype", ctypes.c_int), ("score", ctypes.c_int)]
 
 
 class GemmError(RuntimeError):
@@ -129,6 +143,15 @@ SIGNATURES = [
     ("gemm_w4_plan_destroy", None, [_p]),
     ("gemm_w4_plan_describe", ctypes.c_int, [_p, ctypes.c_char_p, ctypes.c_size_t]),
     ("gemm_w4_run", ctypes.c_int, [_p, _p, _p, _p, _p, _p, _p, _p]),
+    ("gemm_rms_norm", ctypes.c_int, [ctypes.POINTER(gemm_norm_problem), _p, _p, _p, _p, _p, _p, _p]),
+    ("gemm_rms_norm_i8", ctypes.c_int, [ctypes.POINTER(gemm_norm_problem), _p, _p, _p, _p, _p, _p, _p]),
+    ("gemm_i8_quantize", ctypes.c_int, [_p, ctypes.c_int, _i64, _i64, _i64, _p, _i64, _p, _p]),
+    ("gemm_rms_norm_grad_workspace", ctypes.c_int,
+     [ctypes.POINTER(gemm_norm_problem), ctypes.POINTER(ctypes.c_size_t)]),
+    ("gemm_rms_norm_grad", ctypes.c_int,
+     [ctypes.POINTER(gemm_norm_problem), _p, _p, _p, _p, _p, _p, _p, _p, ctypes.c_size_t, _p]),
+    ("gemm_route", ctypes.c_int, [ctypes.POINTER(gemm_route_problem), _p, _p, _p, _p, _p]),
+    ("gemm_route_grad", ctypes.c_int, [ctypes.POINTER(gemm_route_problem), _p, _p, _p, _p, _p]),
     ("gemm_status_string", ctypes.c_char_p, [ctypes.c_int]),
     ("gemm_last_error", ctypes.c_char_p, []),
 ]

@@ -70,7 +70,8 @@ extern "C" {
 typedef enum gemm_dtype {
     GEMM_F16 = 0,   /* IEEE binary16 storage, fp32 accumulate */
     GEMM_BF16 = 1,  /* bfloat16 storage, fp32 accumulate */
-    GEMM_I8 = 2     /* int8 A and B, int32 accumulate, int32 C and D (below) */
+    GEMM_I8 = 2,    /* int8 A and B, int32 accumulate, int32 C and D (below) */
+    GEMM_F32 = 3    /* of the row operators and the scaled int8 product alone, where they say so */
 } gemm_dtype;
 
 /* GEMM_I8 (FlagGems "Hygon optimization", section "DUMMA matrix instruction
@@ -414,6 +415,100 @@ gemm_status gemm_w4_plan_describe(const gemm_w4_plan* plan, char* buf, size_t le
  * workspace; capturable in a graph. */
 gemm_status gemm_w4_run(const gemm_w4_plan* plan, const void* X, const void* W, const void* S, const void* Z,
                         const void* expert_ids, void* Y, void* stream);
+
+/* ---- RMS norm, and rows in 8 bits.
+ *
+ * For each of R rows of K values, h = x + r in fp32, rounded to the rows' type
+ * (with has_residual; else h is x), n = sqrt(mean_k h_k^2 + eps), and
+ *
+ *     gemm_rms_norm      y_k = h_k w_k / n, rounded once to the rows' type
+ *     gemm_rms_norm_i8   the same values as int8 with a scale for each row
+ *     gemm_i8_quantize   x as int8 with a scale for each row
+ *
+ * Rows v in 8 bits: scale = max_k |v_k| / 127 in fp32 and q_k = v_k / scale,
+ * divided in fp32 and rounded to the nearest integer, halves to even, so that
+ * |q_k| <= 127 and v_k is about q_k scale.  A row of zeros (or of values below
+ * 127 x 2^-150) has the scale 0 and zeros; a row with an infinity or a NaN has
+ * the scale NaN and zeros.  They are the operands of gemm_i8_run.
+ *
+ * Rows are fp16 or bf16, K contiguous elements each, at any element-aligned
+ * address and any row strides (at least K for outputs; inputs may share rows);
+ * w is of the rows' type or fp32.  Sums, n and scales are fp32.  Results are
+ * bitwise reproducible.  No outputs may overlap anything.  rstd: NULL, or R
+ * floats that receive 1 / n for the gradient.  No workspace; capturable. */
+typedef struct gemm_norm_problem {
+    int64_t R, K;               /* each up to 2^31 - 4096 */
+    int64_t sx, sr;             /* row strides in elements: x and r, */
+    int64_t sh, sy;             /* h, and y or q (gradient: see there) */
+    gemm_dtype dtype;           /* of the rows: GEMM_F16 or GEMM_BF16 */
+    gemm_dtype weight;          /* of w: dtype or GEMM_F32 */
+    int32_t has_residual;
+    float eps;                  /* above 0 */
+} gemm_norm_problem;
+
+gemm_status gemm_rms_norm(const gemm_norm_problem* prob, const void* x, const void* r, const void* w, void* h, void* y,
+                          float* rstd, void* stream);
+gemm_status gemm_rms_norm_i8(const gemm_norm_problem* prob, const void* x, const void* r, const void* w, void* h,
+                             int8_t* q, float* scale, void* stream);
+gemm_status gemm_i8_quantize(const void* x, gemm_dtype dtype, int64_t R, int64_t K, int64_t sx, int8_t* q, int64_t sq,
+                             float* scale, void* stream);
+
+/* The gradients of gemm_rms_norm, from dy, the stream h that was normalized (x
+ * without a residual), w and rstd:
+ *     dx = w dy / n - h (sum_k w dy h) / (K n^3) + dh        (x's, and r's)
+ *     dw = sum over the rows of dy h / n                     (of w's type)
+ * dh (with has_residual, required then): the gradient of h as an output.
+ * Strides: sy of dy, sr of dh, sh of h, sx of dx.  dw may be NULL: not wanted,
+ * and no workspace needed; else workspace is 16-byte aligned, with no
+ * preparation, for one call at a time, overlapping nothing. */
+gemm_status gemm_rms_norm_grad_workspace(const gemm_norm_problem* prob, size_t* bytes);
+gemm_status gemm_rms_norm_grad(const gemm_norm_problem* prob, const void* dy, const void* dh, const void* h,
+                               const void* w, const float* rstd, void* dx, void* dw, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* ---- Routing of tokens to experts.
+ *
+ * For each of R rows of E logits l:
+ *     p = softmax(l) or sigmoid(l);  c = p + bias (c = p without one)
+ *  - the experts lie in `groups` runs of E / groups; a group's strength is the
+ *    sum of its best group_best (1 or 2) c; the top_groups strongest take part;
+ *  - ids: the `top` experts of largest c among these, largest first, and the
+ *    lowest index first where c (or strengths) are equal;
+ *  - weights: scale p of each, divided by the sum of the chosen p with
+ *    renormalize.  The bias moves the choice alone.
+ * What is compared is exact: the logits themselves without a bias (the scores
+ * have their order), else scores in 64 bits wherever fp32 could confuse two.
+ * Weights are computed and written in fp32.
+ *
+ * An expert whose logit or bias is -infinity or NaN is never chosen (and adds
+ * nothing to a group's strength); where fewer than `top` are left, the last ids
+ * are -1 with the weight 0, which gemm_group_rows and gemm_w4_run take as no
+ * group.  A row with a NaN logit has NaN for the weights of its chosen experts.
+ *
+ * gemm_route_grad: dlogits (R x E, the logits' type) from dweights (R x top),
+ * the ids that were chosen, and the logits.  The choice has no gradient, nor
+ * has the bias.  An id outside [0, E) adds nothing, an id given twice counts
+ * twice.  logits: rows sl elements apart; all other arrays are contiguous.
+ * Outputs overlap nothing.  No workspace; capturable in a graph. */
+typedef enum gemm_score { GEMM_SCORE_SOFTMAX = 0, GEMM_SCORE_SIGMOID = 1 } gemm_score;
+
+typedef struct gemm_route_problem {
+    int64_t R;                  /* up to 2^31 - 4096 */
+    int64_t sl;                 /* row stride of the logits, elements */
+    int32_t E;                  /* 1 to 1024 */
+    int32_t top;                /* 1 to 64, at most the experts of top_groups groups */
+    int32_t groups, top_groups; /* groups divide E, at most 64; 1 and 1: no groups */
+    int32_t group_best;         /* 1 or 2 */
+    int32_t has_bias, renormalize;
+    float scale;
+    gemm_dtype dtype;           /* of the logits: GEMM_F16, GEMM_BF16 or GEMM_F32 */
+    gemm_score score;
+} gemm_route_problem;
+
+gemm_status gemm_route(const gemm_route_problem* prob, const void* logits, const float* bias, float* weights,
+                       int32_t* ids, void* stream);
+gemm_status gemm_route_grad(const gemm_route_problem* prob, const void* logits, const int32_t* ids,
+                            const float* dweights, void* dlogits, void* stream);
 
 const char* gemm_status_string(gemm_status status);
 

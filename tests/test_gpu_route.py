@@ -1,0 +1,288 @@
+"""Routing and its gradient against 64 bits (GPU).
+
+The ids have to be the oracle's, whatever rounding does.  A weight in fp32
+(steps of 2^-24) goes through an exponential of a difference of logits (one
+rounding of the difference: |difference| steps relative, and one of its own), at
+most 20 additions, two divisions and a product: 2^-18 relative, and 2^-23 for
+every unit that the logits of the chosen are apart."""
+import math
+
+import pytest
+import torch
+
+from dense_tiled_gemm_02_amd import grouped, router
+from test_route import oracle, oracle_grad, scores
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+TINY = 2.0 ** -126
+
+
+def check(l, top, **kw):
+    """The call's ids and weights for the CPU logits l; the ids."""
+    w, ids = router.route(l.cuda(), top, **{k: v.cuda() if torch.is_tensor(v) else v for k, v in kw.items()})
+    assert w.dtype == torch.float32 and ids.dtype == torch.int32 and w.shape == ids.shape == (l.shape[0], top)
+    want, want_ids = oracle(l, top, **kw)
+    assert torch.equal(ids.cpu(), want_ids), (ids.cpu()[(ids.cpu() != want_ids).any(1)][:3], want_ids[(ids.cpu() != want_ids).any(1)][:3])
+    got = w.cpu().double()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    got, want = got.nan_to_num(0.0), want.nan_to_num(0.0)
+    # of the chosen alone (rows with a NaN have been compared: all their weights are)
+    held = l.double().nan_to_num(0.0, 1e4, -1e4).clamp(-1e4, 1e4)
+    picked = held.gather(1, want_ids.long().clamp(min=0))
+    first = picked[:, :1]   # a row without choices has weights of zero, to the bit
+    picked = torch.where(want_ids >= 0, picked, first)
+    most = picked if kw.get("renormalize", True) else held
+    apart = most.max(1).values[:, None] - picked.min(1).values[:, None]
+    assert bool(((got - want).abs() <= want.abs() * (2.0 ** -18 + apart * 2.0 ** -23) + TINY).all()), (got - want).abs().max()
+    return want_ids
+
+
+def random_logits(R, E, dt, seed, scale=1.5):
+    gen = torch.Generator().manual_seed(seed)
+    return (torch.randn(R, E, generator=gen) * scale).to(TYPES[dt])
+
+
+def random_bias(E, seed, scale=0.05):
+    return torch.randn(E, generator=torch.Generator().manual_seed(1000 + seed)) * scale
+
+
+@pytest.mark.parametrize("E", [1, 2, 3, 15, 16, 17, 33, 64, 65, 100, 128, 129, 200, 256, 257, 300, 512, 513, 1000, 1024])
+@pytest.mark.parametrize("dt", TYPES)
+def test_sizes(E, dt):
+    print("sizes", E, dt, flush=True)
+    for i, top in enumerate(sorted({1, min(2, E), min(8, E), min(17, E), min(64, E)})):
+        for score in ("softmax", "sigmoid"):
+            l = random_logits(37, E, dt, E + i)
+            check(l, top, score=score, renormalize=i % 2 == 0, scale=1.0 + i)
+            check(l, top, score=score, renormalize=i % 2 == 1, scale=2.5, bias=random_bias(E, i))
+
+
+@pytest.mark.parametrize("E, groups", [(8, 2), (12, 4), (16, 16), (30, 5), (64, 8), (96, 3), (160, 8), (256, 8), (256, 16),
+                                       (256, 2), (256, 32), (320, 10), (512, 16), (640, 64), (1024, 8), (64, 64)])
+@pytest.mark.parametrize("dt", TYPES)
+def test_groups(E, groups, dt):
+    print("groups", E, groups, dt, flush=True)
+    for i, kept in enumerate(sorted({1, (groups + 1) // 2, groups})):
+        top = min(8, kept * (E // groups))
+        for best in (1, 2):
+            for score in ("softmax", "sigmoid"):
+                l = random_logits(33, E, dt, E + i)
+                kw = dict(score=score, groups=groups, top_groups=kept, group_best=best, renormalize=i != 1)
+                check(l, top, **kw)
+                check(l, top, bias=random_bias(E, best), **kw)
+
+
+def test_equal_logits_take_the_lowest_index():
+    for dt in TYPES.values():
+        for E, groups in ((7, 1), (64, 1), (64, 8), (256, 8), (600, 4)):
+            print("ties", dt, E, groups, flush=True)
+            l = torch.zeros(5, E, dtype=dt)
+            l[1, E // 2:] = 1
+            l[2, ::3] = 2
+            l[3] = -5
+            l[4] = torch.arange(E) % 4
+            for bias in (None, torch.zeros(E), torch.full((E,), 0.25)):
+                for score in ("softmax", "sigmoid"):
+                    for best in (1, 2):
+                        check(l, 4, score=score, bias=bias, groups=groups, top_groups=min(2, groups), group_best=best)
+
+
+def test_scores_that_fp32_cannot_tell_apart():
+    """Pairs of experts whose biased scores differ by 1e-9 or less, the lower index now the larger, now the smaller."""
+    gen = torch.Generator().manual_seed(4)
+    R, E = 400, 64
+    for score in ("sigmoid", "softmax"):
+        l = torch.randn(R, E, generator=gen) * 0.3
+        bias = torch.zeros(E)
+        bias[1::2] = 0.0625
+        for r in range(R):
+            # expert 2 i + 1 with its bias next to expert 2 i without: solved in 64 bits, then rounded
+            p = scores(l[r:r + 1].double(), score)[0]
+            i = r % (E // 2)
+            if score == "sigmoid":
+                want = float(p[2 * i]) - 0.0625 + (r % 7 - 3) * 1e-10
+                l[r, 2 * i + 1] = math.log(want / (1 - want))
+                l[r, 2 * i] += 2.0   # both among the best
+                want = float(torch.sigmoid(l[r, 2 * i].double())) - 0.0625 + (r % 7 - 3) * 1e-10
+                l[r, 2 * i + 1] = math.log(want / (1 - want))
+        check(l, 6, score=score, bias=bias)
+        check(l, 6, score=score, bias=bias, groups=8, top_groups=3, group_best=2)
+    # fp32 scores of 1 - 2^-25 and closer to 1 round to 1: only 64 bits order them
+    l = (torch.arange(64).float().flip(0) * 0.01 + 17.5).repeat(3, 1)
+    check(l, 8, score="sigmoid", bias=torch.full((64,), 0.5))
+    check(l, 8, score="sigmoid", groups=8, top_groups=2, group_best=2)
+
+
+def test_masked_experts_and_rows():
+    for dt in TYPES.values():
+        low = torch.finfo(dt).min
+        for E, groups in ((12, 1), (64, 8), (256, 8), (500, 5)):
+            print("masks", dt, E, groups, flush=True)
+            gen = torch.Generator().manual_seed(E)
+            l = torch.randn(9, E, generator=gen).to(dt)
+            l[0] = -math.inf
+            l[1, 3:] = -math.inf
+            l[2, torch.rand(E, generator=gen) < 0.5] = -math.inf
+            l[3] = low
+            l[4, : E // 2] = low
+            l[5, 1] = math.nan
+            l[6] = math.nan
+            l[7, 2] = l[7, 5] = math.inf
+            l[8, E - 1] = torch.finfo(dt).max
+            bias = random_bias(E, 1)
+            bias[4] = -math.inf
+            bias[6] = math.nan
+            ahead = bias.clone()
+            ahead[7] = math.inf
+            for b in (None, bias, ahead):
+                for score in ("softmax", "sigmoid"):
+                    for renormalize in (True, False):
+                        ids = check(l, 6, score=score, bias=b, groups=groups, top_groups=min(3, groups),
+                                    group_best=2 if groups == 8 else 1, renormalize=renormalize)
+                        assert bool((ids[0] == -1).all())
+            # every expert masked by the bias
+            check(l, 2, score="sigmoid", bias=torch.full((E,), -math.inf))
+
+
+def test_scores_far_from_one():
+    """Shares of scores that fp32 cannot hold."""
+    gen = torch.Generator().manual_seed(2)
+    for level in (-20.0, -90.0, -200.0, 90.0):
+        l = torch.randn(20, 40, generator=gen) + level
+        check(l, 5, score="sigmoid")
+        check(l, 5, score="softmax")
+    l = torch.randn(20, 40, generator=gen) * 100
+    check(l, 5)
+    check(l, 5, renormalize=False)
+
+
+def gradients(l, ids, dw, score, renormalize, scale, got, dt):
+    ref = oracle_grad(dw, l, ids, score, renormalize, scale)
+    real = ids >= 0
+    at = ids.long().clamp(min=0)
+    p = scores(l, score)
+    g = (dw.double() * scale).abs() * real
+    if renormalize:
+        u = p.gather(1, at) * real
+        u = u / u.sum(1, keepdim=True).clamp(min=1e-300)
+        size = torch.zeros_like(p).scatter_add_(1, at, u * (g + (g * u).sum(1, keepdim=True)))
+    else:
+        size = torch.zeros_like(p).scatter_add_(1, at, p.gather(1, at) * g) + p * (p.gather(1, at) * g).sum(1, keepdim=True)
+    picked = torch.where(real, l.double().gather(1, at), l.double().max(1, keepdim=True).values)
+    apart = (l.double().max(1).values - picked.min(1).values)[:, None]
+    half = 0 if dt == "f32" else torch.finfo(TYPES[dt]).eps / 2
+    small = torch.finfo(TYPES[dt]).tiny * torch.finfo(TYPES[dt]).eps
+    bound = ref.abs() * half + size * (2.0 ** -17 + apart * 2.0 ** -22) + small
+    assert bool(((got.cpu().double() - ref).abs() <= bound).all()), ((got.cpu().double() - ref).abs() - bound).max()
+
+
+@pytest.mark.parametrize("E", [1, 3, 16, 64, 100, 256, 300, 1024])
+@pytest.mark.parametrize("dt", TYPES)
+def test_gradients(E, dt):
+    print("gradients", E, dt, flush=True)
+    for top in sorted({1, min(8, E), min(20, E), min(64, E)}):
+        for score in ("softmax", "sigmoid"):
+            for renormalize in (True, False):
+                l = random_logits(35, E, dt, E + top)
+                dw = torch.randn(35, top, generator=torch.Generator().manual_seed(top))
+                leaf = l.cuda().requires_grad_()
+                w, ids = router.route(leaf, top, score=score, renormalize=renormalize, scale=1.5)
+                assert not ids.requires_grad
+                got, = torch.autograd.grad(w, leaf, dw.cuda())
+                assert got.dtype == l.dtype and got.shape == l.shape
+                gradients(l, ids.cpu(), dw, score, renormalize, 1.5, got, dt)
+                again = router.route_grad(dw.cuda(), leaf.detach(), ids, score=score, renormalize=renormalize, scale=1.5)
+                assert torch.equal(again, got)
+
+
+def test_gradients_with_masks_and_odd_ids():
+    l = random_logits(6, 40, "f32", 3)
+    l[0] = -math.inf
+    l[1, 2:] = -math.inf
+    l[2, 7] = math.nan
+    for score in ("softmax", "sigmoid"):
+        for renormalize in (True, False):
+            leaf = l.cuda().requires_grad_()
+            w, ids = router.route(leaf, 4, score=score, renormalize=renormalize)
+            dw = torch.randn(6, 4, generator=torch.Generator().manual_seed(5))
+            got, = torch.autograd.grad(w, leaf, dw.cuda())
+            assert bool((got[0] == 0).all()) and bool((got[1, 2:] == 0).all()) and float(got[2, 7]) == 0.0
+            rows = [1, 3, 4, 5]
+            gradients(l[rows], ids.cpu()[rows], dw[rows], score, renormalize, 1.0, got[rows], "f32")
+            # ids of the caller's own: outside the experts (no part), and the same one twice (both count)
+            ids = torch.tensor([[5, -1, 40, 9]] * 3 + [[3, 3, 8, -2]] * 3, dtype=torch.int32)
+            clean = torch.where((ids < 0) | (ids >= 40), -1, ids)
+            got = router.route_grad(dw.cuda(), l.cuda(), ids.cuda(), score=score, renormalize=renormalize)
+            gradients(l[3:], clean[3:], dw[3:], score, renormalize, 1.0, got[3:], "f32")
+
+
+def test_views_and_many_rows():
+    base = random_logits(3000, 90, "bf16", 1)
+    wide = base.cuda()
+    check(base[:200, 7:80], 5, score="sigmoid", bias=random_bias(73, 1))
+    w, ids = router.route(wide[:, 7:80], 5)
+    w2, ids2 = router.route(wide[:, 7:80].contiguous(), 5)
+    assert torch.equal(w, w2) and torch.equal(ids, ids2)
+    one = wide[3:4, 7:80].expand(50, 73)
+    w3, ids3 = router.route(one, 5)
+    assert torch.equal(w3, w2[3:4].expand(50, 5)) and torch.equal(ids3, ids2[3:4].expand(50, 5))
+    leaf = wide[:, 7:80].detach().requires_grad_()
+    w, ids = router.route(leaf, 5)
+    dw = torch.randn(3000, 5, device="cuda")
+    assert torch.equal(torch.autograd.grad(w, leaf, dw)[0], router.route_grad(dw, wide[:, 7:80].contiguous(), ids))
+    leaf = wide[:, :64].float().requires_grad_()
+    w, ids = router.route(leaf, 3, renormalize=False)
+    got, = torch.autograd.grad(w.sum(), leaf)   # a gradient expanded from one value
+    assert torch.equal(got, router.route_grad(torch.ones(3000, 3, device="cuda"), leaf.detach(), ids, renormalize=False))
+
+
+def test_no_rows():
+    l = torch.empty(0, 8, device="cuda", requires_grad=True)
+    w, ids = router.route(l, 3)
+    assert w.shape == ids.shape == (0, 3)
+    assert torch.autograd.grad(w, l, torch.empty_like(w))[0].shape == (0, 8)
+
+
+def test_the_ids_group_rows():
+    l = random_logits(500, 24, "f32", 8)
+    l[10] = -math.inf
+    w, ids = router.route(l.cuda(), 3)
+    offsets, order = grouped.group_rows(ids.reshape(-1), 24)
+    counts = torch.bincount(ids.cpu().reshape(-1).clamp(min=-1) + 1, minlength=25)
+    assert torch.equal(offsets.cpu().diff().long(), counts[1:]) and int(offsets[-1]) == 1500 - int(counts[0])
+    assert int(counts[0]) == 3
+
+
+def test_another_stream_and_a_captured_step():
+    l = random_logits(4000, 128, "bf16", 1).cuda()
+    want = router.route(l, 4)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = router.route(l, 4, stream=s)
+    s.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+    leaf = l.clone().requires_grad_()
+    dw = torch.randn(4000, 4, device="cuda")
+
+    def step():
+        w, ids = router.route(leaf, 4, score="sigmoid", groups=8, top_groups=3, group_best=2)
+        return [w.detach(), ids, torch.autograd.grad(w, leaf, dw)[0]]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for i in range(3):
+        with torch.no_grad():
+            leaf.copy_(random_logits(4000, 128, "bf16", 10 + i))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in captured]
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
