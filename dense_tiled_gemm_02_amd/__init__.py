@@ -83,6 +83,11 @@ class gemm_norm_problem(ctypes.Structure):
                 ("dtype", ctypes.c_int), ("weight", ctypes.c_int), ("has_residual", _i32), ("eps", ctypes.c_float)]
 
 
+class gemm_i8_problem(ctypes.Structure):
+    _fields_ = [("M", _i64), ("N", _i64), ("K", _i64), ("sx", _i64), ("sw", _i64), ("sy", _i64),
+                ("out", ctypes.c_int), ("has_bias", _i32)]
+
+
 class gemm_route_problem(ctypes.Structure):
     _fields_ = [("R", _i64), ("sl", _i64), ("E", _i32), ("top", _i32), ("groups", _i32), ("top_groups", _i32),
                 ("group_best", _i32), ("has_bias", _i32), ("renormalize", _i32), ("scale", ctypes.c_float),
@@ -150,6 +155,12 @@ SIGNATURES = [
      [ctypes.POINTER(gemm_norm_problem), ctypes.POINTER(ctypes.c_size_t)]),
     ("gemm_rms_norm_grad", ctypes.c_int,
      [ctypes.POINTER(gemm_norm_problem), _p, _p, _p, _p, _p, _p, _p, _p, ctypes.c_size_t, _p]),
+    ("gemm_i8_plan_create", ctypes.c_int, [ctypes.POINTER(gemm_i8_problem), ctypes.c_int, ctypes.POINTER(_p)]),
+    ("gemm_i8_plan_create_for", ctypes.c_int,
+     [ctypes.POINTER(gemm_i8_problem), ctypes.POINTER(gemm_device_info), ctypes.POINTER(_p)]),
+    ("gemm_i8_plan_destroy", None, [_p]),
+    ("gemm_i8_plan_describe", ctypes.c_int, [_p, ctypes.c_char_p, ctypes.c_size_t]),
+    ("gemm_i8_run", ctypes.c_int, [_p, _p, _p, _p, _p, _p, _p, _p]),
     ("gemm_route", ctypes.c_int, [ctypes.POINTER(gemm_route_problem), _p, _p, _p, _p, _p]),
     ("gemm_route_grad", ctypes.c_int, [ctypes.POINTER(gemm_route_problem), _p, _p, _p, _p, _p]),
     ("gemm_status_string", ctypes.c_char_p, [ctypes.c_int]),

@@ -35,7 +35,8 @@ SOURCES = ["api.cpp", "api_mx.cpp", "gemm_tile.hip", "gemm_dma.hip", "gemm_dma_m
            "api_grouped.cpp", "gemm_grouped_rows.hip", "gemm_grouped_reduce.hip", "gemm_grouped_any.hip",
            "gemm_grouped_odd.hip", "gemm_grouped_few.hip", "gemm_grouped_mixed.hip",
            "sum_parts.hip", "group_rows.hip", "api_w4.cpp", "gemm_w4.hip",
-           "api_rows.cpp", "rms_norm.hip", "api_route.cpp", "route.hip"]
+           "api_rows.cpp", "rms_norm.hip", "api_route.cpp", "route.hip",
+           "api_i8.cpp", "i8_scaled.hip", "i8_few.hip", "i8_any.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 COMMON = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=" + ARCH,

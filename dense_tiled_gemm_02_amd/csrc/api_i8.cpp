@@ -1,0 +1,238 @@
+// C ABI of the int8 products with scales: validation, variant choice and
+// launch.  Declarations and the contract are in include/gemm.h.
+#include <hip/hip_runtime.h>
+#include <stdarg.h>
+#include <stdint.h>
+#include <stdio.h>
+
+#include <new>
+
+#include "../../include/gemm.h"
+#include "api_internal.h"
+#include "kernels_i8.h"
+
+struct gemm_i8_plan {
+    gemm_i8_problem prob;
+    int out;                          // kOutF16, kOutBF16, kOutF32
+    const dtg::I8TileEntry* tile;     // one of these two, or neither: the kernel for any address
+    const dtg::I8FewEntry* few;
+    int64_t tiles_m, tiles_n;
+    int group_m, xcds;
+};
+
+namespace {
+
+gemm_status fail(gemm_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+gemm_status fail(gemm_status st, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return dtg::record_error(st, buf);
+}
+
+constexpr int64_t kMaxRows = int64_t(1) << 27;        // of X and W: the grids of the smallest tiles
+constexpr int64_t kMaxOutputs = int64_t(1) << 35;
+constexpr int64_t kMaxK = int64_t(1) << 17;           // 2^17 products of 2^14 make 2^31
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Bytes from the first to one past the last of `rows` rows of `cols`, or -1 past 2^60.
+int64_t extent(int64_t rows, int64_t stride, int64_t cols, int64_t size) {
+    if (rows <= 0 || cols <= 0) return 0;
+    const __int128 e = (static_cast<__int128>(rows - 1) * stride + cols) * size;
+    return e > (static_cast<__int128>(1) << 60) ? -1 : static_cast<int64_t>(e);
+}
+
+int out_bytes(const gemm_i8_problem* p) { return p->out == GEMM_F32 ? 4 : 2; }
+
+gemm_status validate(const gemm_i8_problem* p) {
+    if (!p) return fail(GEMM_ERR_INVALID_ARG, "problem is NULL");
+    if (p->M < 0 || p->N < 0 || p->K < 0)
+        return fail(GEMM_ERR_INVALID_ARG, "negative size M=%lld N=%lld K=%lld", (long long)p->M, (long long)p->N,
+                    (long long)p->K);
+    if (p->out != GEMM_F16 && p->out != GEMM_BF16 && p->out != GEMM_F32)
+        return fail(GEMM_ERR_INVALID_ARG, "output type %d is none of GEMM_F16, GEMM_BF16, GEMM_F32", (int)p->out);
+    if (p->has_bias != 0 && p->has_bias != 1)
+        return fail(GEMM_ERR_INVALID_ARG, "has_bias must be 0 or 1, got %d", (int)p->has_bias);
+    if (p->M > kMaxRows || p->N > kMaxRows || p->M * p->N > kMaxOutputs)
+        return fail(GEMM_ERR_UNSUPPORTED, "M and N above 2^27 or more than 2^35 outputs are not supported");
+    if (p->K >= kMaxK)
+        return fail(GEMM_ERR_UNSUPPORTED, "K=%lld: sums of 2^17 products and more can pass int32", (long long)p->K);
+    if (p->sx < 0 || p->sw < 0 || p->sy < 0) return fail(GEMM_ERR_UNSUPPORTED, "negative stride");
+    if (extent(p->M, p->sx, p->K, 1) < 0 || extent(p->N, p->sw, p->K, 1) < 0 || extent(p->M, p->sy, p->N, 4) < 0)
+        return fail(GEMM_ERR_INVALID_ARG, "strides reach past 2^60 bytes");
+    if (p->M > 1 && p->sy < p->N)
+        return fail(GEMM_ERR_INVALID_ARG, "Y row stride %lld < N=%lld makes output rows overlap", (long long)p->sy,
+                    (long long)p->N);
+    return GEMM_OK;
+}
+
+// Rows 16 bytes apart and whole chunks of 16 k: the direct-to-LDS kernels.
+bool chunked(const gemm_i8_problem* p) {
+    return p->K > 0 && p->K % 16 == 0 && p->sx % 16 == 0 && p->sw % 16 == 0;
+}
+
+// 32-bit offsets of `rows` rows from a rebased descriptor.
+bool near(int64_t rows, int64_t stride, int64_t K) { return rows * stride + K < (int64_t(1) << 31) - 4096; }
+
+const dtg::I8FewEntry* pick_few(const gemm_i8_problem* p, const gemm_device_info* dev) {
+    if (p->M > 64) return nullptr;
+    const int mb = p->M <= 16 ? 1 : p->M <= 32 ? 2 : 4;
+    // two column blocks where one leaves every CU more than a workgroup
+    const int nb = mb > 1 || cdiv(p->N, 16) > dev->cu_count ? 2 : 1;
+    int n = 0;
+    const dtg::I8FewEntry* t = dtg::i8_few_table(&n);
+    for (int i = 0; i < n; ++i)
+        if (t[i].mb == mb && t[i].nb == nb && t[i].rows >= p->M && near(16 * nb, p->sw, p->K) && near(64, p->sx, p->K))
+            return &t[i];
+    return nullptr;
+}
+
+const dtg::I8TileEntry* pick_tile(const gemm_i8_problem* p, const gemm_device_info* dev, int out) {
+    // rounds of workgroups times a tile's cost relative to 256 x 256, as for the dense tiles
+    static const struct { int bm, bn, stages, per_cu; double cost; } ladder[] = {
+        {256, 256, 2, 1, 1.0}, {256, 128, 3, 1, 0.64}, {128, 256, 3, 1, 0.64},
+        {128, 128, 4, 1, 0.43}, {128, 128, 2, 2, 0.68}, {64, 64, 4, 2, 0.27}};
+    int n = 0, best = -1;
+    double best_t = 0.0;
+    const dtg::I8TileEntry* t = dtg::i8_scaled_table(&n);
+    for (int i = 0; i < n; ++i) {
+        if (t[i].out != out || !near(t[i].bm, p->sx, p->K) || !near(t[i].bn, p->sw, p->K)) continue;
+        for (const auto& c : ladder) {
+            if (c.bm != t[i].bm || c.bn != t[i].bn || c.stages != t[i].stages) continue;
+            const double cost = static_cast<double>(cdiv(cdiv(p->M, c.bm) * cdiv(p->N, c.bn), int64_t(dev->cu_count) * c.per_cu)) * c.cost;
+            if (best < 0 || cost < best_t) best = i, best_t = cost;
+        }
+    }
+    return best < 0 ? nullptr : &t[best];
+}
+
+gemm_status plan_impl(const gemm_i8_problem* given, const gemm_device_info* dev, gemm_i8_plan** out) {
+    if (!out) return fail(GEMM_ERR_INVALID_ARG, "out is NULL");
+    *out = nullptr;
+    const gemm_status st = validate(given);
+    if (st != GEMM_OK) return st;
+    gemm_i8_problem seen = *given;   // without the strides that no access uses
+    if (seen.M <= 1) seen.sx = 0;
+    if (seen.N <= 1) seen.sw = 0;
+    const gemm_i8_problem* const p = &seen;
+    if (!dev || dev->cu_count <= 0) return fail(GEMM_ERR_INVALID_ARG, "device info missing, or without CUs");
+    gemm_i8_plan* pl = new (std::nothrow) gemm_i8_plan();
+    if (!pl) return fail(GEMM_ERR_INVALID_ARG, "out of host memory");
+    pl->prob = *p;
+    pl->out = p->out == GEMM_F32 ? dtg::kOutF32 : p->out == GEMM_BF16 ? dtg::kOutBF16 : dtg::kOutF16;
+    if (chunked(p)) {
+        pl->few = pick_few(p, dev);
+        if (!pl->few) pl->tile = pick_tile(p, dev, pl->out);
+    }
+    if (pl->tile) {
+        pl->tiles_m = cdiv(p->M, pl->tile->bm);
+        pl->tiles_n = cdiv(p->N, pl->tile->bn);
+        pl->group_m = 8;
+        pl->xcds = dev->xcd_count > 0 ? dev->xcd_count : 1;
+    } else {
+        pl->tiles_m = cdiv(p->M, pl->few ? 16 * pl->few->mb : 64);
+        pl->tiles_n = cdiv(p->N, pl->few ? 16 * pl->few->nb : 64);
+    }
+    *out = pl;
+    return GEMM_OK;
+}
+
+struct Operand {
+    const char* name;
+    const void* p;
+    int64_t bytes;
+    int align;
+};
+
+}  // namespace
+
+extern "C" {
+
+gemm_status gemm_i8_plan_create_for(const gemm_i8_problem* prob, const gemm_device_info* info, gemm_i8_plan** out) {
+    return plan_impl(prob, info, out);
+}
+
+gemm_status gemm_i8_plan_create(const gemm_i8_problem* prob, int device, gemm_i8_plan** out) {
+    if (out) *out = nullptr;
+    gemm_status st = validate(prob);
+    if (st != GEMM_OK) return st;
+    gemm_device_info info;
+    st = dtg::cached_device_info(device, &info);
+    if (st != GEMM_OK) return st;
+    return plan_impl(prob, &info, out);
+}
+
+void gemm_i8_plan_destroy(gemm_i8_plan* plan) { delete plan; }
+
+gemm_status gemm_i8_plan_describe(const gemm_i8_plan* plan, char* buf, size_t len) {
+    if (!plan || !buf || len == 0) return fail(GEMM_ERR_INVALID_ARG, "plan or buf is NULL");
+    snprintf(buf, len, "kernel=%s grid=%lldx%lld", plan->tile ? plan->tile->name : plan->few ? plan->few->name : "i8_any_kernel",
+             (long long)plan->tiles_m, (long long)plan->tiles_n);
+    return GEMM_OK;
+}
+
+gemm_status gemm_i8_run(const gemm_i8_plan* plan, const int8_t* X, const float* x_scale, const int8_t* W, const float* w_scale,
+                        const void* bias, void* Y, void* stream) {
+    if (!plan) return fail(GEMM_ERR_INVALID_ARG, "plan is NULL");
+    const gemm_i8_problem& p = plan->prob;
+    if (!p.has_bias && bias) return fail(GEMM_ERR_INVALID_ARG, "bias given but the problem has has_bias = 0");
+    if (p.M == 0 || p.N == 0) return GEMM_OK;
+    const int size = out_bytes(&p);
+    const Operand y = {"Y", Y, extent(p.M, p.sy, p.N, size), size};
+    const Operand in[5] = {{"X", X, extent(p.M, p.sx, p.K, 1), 1},
+                           {"W", W, extent(p.N, p.sw, p.K, 1), 1},
+                           {"x_scale", x_scale, p.M * 4, 4},
+                           {"w_scale", w_scale, p.N * 4, 4},
+                           {"bias", bias, p.has_bias ? p.N * size : 0, size}};
+    if (!Y) return fail(GEMM_ERR_INVALID_ARG, "Y is NULL");
+    if (reinterpret_cast<uintptr_t>(Y) % size) return fail(GEMM_ERR_UNSUPPORTED, "Y must be aligned to its element size");
+    for (const Operand& o : in) {
+        if (o.bytes == 0) continue;
+        if (!o.p) return fail(GEMM_ERR_INVALID_ARG, "%s is NULL", o.name);
+        const uintptr_t a = reinterpret_cast<uintptr_t>(o.p), b = reinterpret_cast<uintptr_t>(y.p);
+        if (a % o.align) return fail(GEMM_ERR_UNSUPPORTED, "%s must be aligned to its element size", o.name);
+        if (a < b + y.bytes && b < a + o.bytes) return fail(GEMM_ERR_INVALID_ARG, "Y overlaps %s", o.name);
+    }
+    const dtg::ScaledI8 scales = {x_scale, w_scale, p.has_bias ? bias : nullptr};
+    const hipStream_t on = static_cast<hipStream_t>(stream);
+    const bool aligned = reinterpret_cast<uintptr_t>(X) % 16 == 0 && reinterpret_cast<uintptr_t>(W) % 16 == 0;
+    hipError_t err;
+    if (plan->tile && aligned) {
+        dtg::ScaledArgs a = {};
+        a.A = reinterpret_cast<const uint16_t*>(X);
+        a.B = reinterpret_cast<const uint16_t*>(W);
+        a.D = static_cast<uint16_t*>(Y);
+        a.M = static_cast<int32_t>(p.M);
+        a.N = static_cast<int32_t>(p.N);
+        a.K = static_cast<int32_t>(p.K / 2);
+        a.num_pid_m = static_cast<int32_t>(plan->tiles_m);
+        a.num_pid_n = static_cast<int32_t>(plan->tiles_n);
+        a.group_m = plan->group_m;
+        a.xcds = plan->xcds;
+        a.splits = 1;
+        a.lda = p.M > 1 ? p.sx / 2 : a.K;   // of one row: none is taken
+        a.sbn = p.N > 1 ? p.sw / 2 : a.K;
+        a.sak = a.ldb = 1;
+        a.ldd = p.sy;
+        a.s = scales;
+        err = plan->tile->launch(a, plan->tiles_m * plan->tiles_n, on);
+    } else {
+        dtg::I8RowsArgs a = {};
+        a.X = X;
+        a.W = W;
+        a.Y = Y;
+        a.s = scales;
+        a.M = static_cast<int32_t>(p.M);
+        a.N = static_cast<int32_t>(p.N);
+        a.K = static_cast<int32_t>(p.K);
+        a.lx = p.sx;
+        a.lw = p.sw;
+        a.ly = p.sy;
+        err = plan->few && aligned ? plan->few->launch[plan->out](a, on) : dtg::launch_i8_any(a, plan->out, on);
+    }
+    return err == hipSuccess ? GEMM_OK : fail(GEMM_ERR_HIP, "launch of the int8 product: %s", hipGetErrorString(err));
+}
+
+}  // extern "C"

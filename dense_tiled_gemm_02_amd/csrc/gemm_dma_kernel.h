@@ -36,7 +36,9 @@
 #include <type_traits>
 
 #include "device_common.h"
+#include "i8_epilogue.h"
 #include "kernels.h"
+#include "kernels_i8.h"
 #include "tile_order.h"
 
 namespace dtg {
@@ -85,8 +87,10 @@ struct OpShape {
 // accumulation and a 16-bit output, or 8-bit integers with int32 accumulation
 // and output.  The int8 operands are staged and read as pairs of bytes (one
 // 16-bit element holds two consecutive k), so the K loop is the same code;
-// K, BK and the strides are in those 16-bit units.
-enum { kElF16 = 0, kElBF16 = 1, kElI8 = 2 };
+// K, BK and the strides are in those 16-bit units.  The last three are the int8
+// operands with a scale for each row of A and column of B, a ScaledArgs, and an
+// output of 16 bits or fp32.
+enum { kElF16 = 0, kElBF16 = 1, kElI8 = 2, kElI8ToF16 = 3, kElI8ToBF16 = 4, kElI8ToF32 = 5 };
 
 // Operation O of NR reads and NL loads issued in one sequence with the loads
 // spread evenly: load j sits at position floor((2 j + 1) (NR + NL) / (2 NL)).
@@ -143,8 +147,9 @@ __device__ __forceinline__ Work slice_work(const KArgs& p) {
 template <int BM, int BN, int BK, int WM, int WN, int MF, int ST, int EL, bool TA, bool TB, bool XCH = false,
           bool NTB = false, bool O32 = false>
 __device__ __forceinline__ void dma_tile_in(uint16_t* const smem, const KArgs& p, const Work& wk) {
-    constexpr bool BF16 = EL == kElBF16;
-    constexpr bool I8 = EL == kElI8;
+    constexpr bool BF16 = EL == kElBF16 || EL == kElI8ToBF16;   // of 16-bit operands and outputs
+    constexpr bool I8 = EL >= kElI8, SCALED = EL > kElI8;
+    constexpr bool OUT32 = EL == kElI8 || EL == kElI8ToF32 || O32;
     constexpr int NW = WM * WN;
     constexpr int TM = BM / WM, TN = BN / WN;
     constexpr int FM = TM / MF, FN = TN / MF;
@@ -163,7 +168,7 @@ __device__ __forceinline__ void dma_tile_in(uint16_t* const smem, const KArgs& p
     // accumulators per lane; above 128 (one wave per SIMD holding a
     // 128 x 128 wave tile) they live in AGPRs, placed there explicitly
     constexpr bool AGPR = FM * FN * AccT<MF>::regs > 128;
-    static_assert(!((I8 || O32) && AGPR), "tiles with 32-bit output keep their accumulators in VGPRs");
+    static_assert(!((I8 || OUT32) && AGPR), "tiles with 32-bit output keep their accumulators in VGPRs");
 
     int tid = threadIdx.x;
     // Stream-K runs this body in a loop: an opaque lane index keeps the
@@ -221,6 +226,27 @@ __device__ __forceinline__ void dma_tile_in(uint16_t* const smem, const KArgs& p
 
     // LDS layout: the ST stages of A, then the ST stages of B.
     const uint32_t smem0 = lds_addr(smem);
+
+    // The tile's scales go to LDS ahead of the ring's loads (whose waits are
+    // then for them, too): 64 floats of A's rows or B's columns to a load, zeros
+    // past the last.
+    __shared__ __attribute__((aligned(16))) float row_col[SCALED ? BM + BN : 4];
+    if constexpr (SCALED) {
+        const ScaledI8& sc = static_cast<const ScaledArgs&>(p).s;
+        static_assert(BM % 64 == 0 && BN % 64 == 0, "scales load 64 at a time");
+#pragma unroll
+        for (int u0 = 0; u0 < (BM + BN) / 64; u0 += NW) {
+            const int u = u0 + wave;
+            if (u < (BM + BN) / 64) {
+                const bool col = u >= BM / 64;
+                const int first = col ? n0 + 64 * (u - BM / 64) : m0 + 64 * u, count = col ? N : M;
+                __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+                    const_cast<float*>((col ? sc.sw : sc.sx) + first), 0,
+                    first < count ? clamp_records(4 * static_cast<int64_t>(count - first)) : 0u, kRsrcWord3);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)(row_col + 64 * u), 4, 4 * lane, 0, 0, 0);
+            }
+        }
+    }
 
     // Buffer descriptors of K step kt: each starts at the tile's first element
     // of that step (k0 and m0 / n0) and ends at the matrix's last element, so
@@ -525,6 +551,8 @@ __device__ __forceinline__ void dma_tile_in(uint16_t* const smem, const KArgs& p
         }
         // no load may still be writing this workgroup's LDS when it exits
         wait_vm<0>();
+    } else if constexpr (SCALED) {
+        wait_vm<0>();   // the scales' loads
     }
     if constexpr (AGPR) agpr_settle();
 
@@ -617,7 +645,34 @@ __device__ __forceinline__ void dma_tile_in(uint16_t* const smem, const KArgs& p
     // 0..3; 32x32x16: run q at columns 8 q + 4 (l / 32) + 0..3).
     constexpr int G = AccT<MF>::regs / 4;
 
-    if constexpr (I8 || O32) {
+    if constexpr (SCALED) {
+        // the sums become outputs in place: see i8_epilogue.h
+        const ScaledI8& sc = static_cast<const ScaledArgs&>(p).s;
+        constexpr int OUT = EL == kElI8ToF32 ? kOutF32 : EL == kElI8ToBF16 ? kOutBF16 : kOutF16;
+        __syncthreads();   // the scales are in LDS
+        float sx[FM];
+#pragma unroll
+        for (int i = 0; i < FM; ++i) sx[i] = row_col[wm * TM + i * MF + (lane % MF)];
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int q = 0; q < G; ++q) {
+                const int c0 = wn * TN + j * MF + 8 * q + 4 * (lane / MF);
+                const f32x4 sw = *reinterpret_cast<const f32x4*>(row_col + BM + c0);
+                f32x4 b = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (sc.bias) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (n0 + c0 + r < N) b[r] = bias_at<OUT>(sc.bias, n0 + c0 + r);
+                }
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[i][j][4 * q + r] = scaled(acc[i][j][4 * q + r], sx[i], sw[r]) + b[r];
+            }
+    }
+
+    if constexpr (OUT32) {
         // 32-bit results (int32, or fp32 with O32): the tile is staged through
         // LDS in P8 passes of BM / P8 rows (16-byte chunks of 4 values at
         // chunk position c ^ (r mod 16) of their row), then each thread adds C
@@ -638,7 +693,7 @@ __device__ __forceinline__ void dma_tile_in(uint16_t* const smem, const KArgs& p
         const bool has_c = p.has_c != 0;
         auto plus = [](uint32_t x, uint32_t c) -> uint32_t {
             if constexpr (O32) return __float_as_uint(__uint_as_float(x) + __uint_as_float(c));
-            else return x + c;
+            else return x + c;   // (with scales there is no addend)
         };
         const bool vec4 = (p.ldd % 4 == 0) && (reinterpret_cast<uintptr_t>(p.D) % 16 == 0) &&
                           (!has_c || ((p.ldc % 4 == 0) && (reinterpret_cast<uintptr_t>(p.C) % 16 == 0)));
@@ -918,6 +973,12 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(KArgs p) {
     dma_tile<BM, BN, BK, WM, WN, MF, ST, kElI8, false, true>(p, slice_work<BK>(p));
 }
 
+// The same with a scale for each row and column (KIND: kOutF16, kOutBF16 or kOutF32).
+template <int BM, int BN, int BK, int WM, int WN, int MF, int ST, int KIND>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_i8s_kernel(ScaledArgs p) {
+    dma_tile<BM, BN, BK, WM, WN, MF, ST, kElI8ToF16 + KIND, false, true>(p, slice_work<BK>(p));
+}
+
 constexpr int kMaxDmaSplits = 64;
 
 template <int BM, int BN, int BK, int WM, int WN, int MF, int ST, bool BF16, bool TA, bool TB>
@@ -944,6 +1005,13 @@ hipError_t launch_dma_sk(const KArgs& a, int64_t grid, hipStream_t stream) {
 template <int BM, int BN, int BK, int WM, int WN, int MF, int ST>
 hipError_t launch_i8(const KArgs& a, int64_t grid, hipStream_t stream) {
     hipLaunchKernelGGL((gemm_i8_kernel<BM, BN, BK, WM, WN, MF, ST>), dim3(static_cast<unsigned>(grid)),
+                       dim3(64 * WM * WN), 0, stream, a);
+    return hipGetLastError();
+}
+
+template <int BM, int BN, int BK, int WM, int WN, int MF, int ST, int KIND>
+hipError_t launch_i8s(const ScaledArgs& a, int64_t grid, hipStream_t stream) {
+    hipLaunchKernelGGL((gemm_i8s_kernel<BM, BN, BK, WM, WN, MF, ST, KIND>), dim3(static_cast<unsigned>(grid)),
                        dim3(64 * WM * WN), 0, stream, a);
     return hipGetLastError();
 }

@@ -466,6 +466,36 @@ gemm_status gemm_rms_norm_grad(const gemm_norm_problem* prob, const void* dy, co
                                const void* w, const float* rstd, void* dx, void* dw, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/* ---- int8 products with a scale for each row of X and row of W.
+ *
+ *     Y[m, n] = (sum_k X[m, k] W[n, k]) x_scale[m] w_scale[n] (+ bias[n])
+ *
+ * X: M x K int8, W: N x K int8 (a weight matrix as it is stored), k contiguous
+ * in both; fp32 scales; Y, and bias if there is one, fp16, bf16 or fp32.  The sum
+ * is exact (int32); it is rounded to fp32, multiplied by x_scale, by w_scale and
+ * added to the bias in fp32, and rounded once to Y's type.  gemm_i8_quantize and
+ * gemm_rms_norm_i8 make the operands.
+ *
+ * Any sizes, strides and alignment run.  With K and the row strides multiples of
+ * 16 and X and W 16-byte aligned, the direct-to-LDS tiles run (M up to 64: kernels
+ * that stream W).  Y may overlap no input.  No workspace; capturable. */
+typedef struct gemm_i8_problem {
+    int64_t M, N, K;            /* M, N up to 2^27 and M N up to 2^35; K below 2^17 */
+    int64_t sx, sw;             /* row strides of X and W, bytes */
+    int64_t sy;                 /* row stride of Y, elements */
+    gemm_dtype out;             /* of Y and bias: GEMM_F16, GEMM_BF16 or GEMM_F32 */
+    int32_t has_bias;
+} gemm_i8_problem;
+
+typedef struct gemm_i8_plan gemm_i8_plan;   /* opaque, immutable after creation */
+
+gemm_status gemm_i8_plan_create(const gemm_i8_problem* prob, int device, gemm_i8_plan** out);
+gemm_status gemm_i8_plan_create_for(const gemm_i8_problem* prob, const gemm_device_info* info, gemm_i8_plan** out);
+void gemm_i8_plan_destroy(gemm_i8_plan* plan);
+gemm_status gemm_i8_plan_describe(const gemm_i8_plan* plan, char* buf, size_t len);
+gemm_status gemm_i8_run(const gemm_i8_plan* plan, const int8_t* X, const float* x_scale, const int8_t* W,
+                        const float* w_scale, const void* bias, void* Y, void* stream);
+
 /* ---- Routing of tokens to experts.
  *
  * For each of R rows of E logits l:

@@ -1,0 +1,176 @@
+"""int8 products with scales against exact sums (GPU).
+
+The sum is exact; rounding it to fp32, two products and the bias's addition are
+four roundings of 2^-24 relative to the product or the result, then one to the
+output's type.  An accumulation error of even one step would be far outside."""
+import pytest
+import torch
+
+import dense_tiled_gemm_02_amd as g
+from dense_tiled_gemm_02_amd import i8
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def int8(shape, seed, lo=-127, hi=127):
+    return torch.randint(lo, hi + 1, shape, generator=torch.Generator().manual_seed(seed), dtype=torch.int8)
+
+
+def operands(M, N, K, out, bias, seed):
+    gen = torch.Generator().manual_seed(seed)
+    x, w = int8((M, K), seed + 1), int8((N, K), seed + 2)
+    sx, sw = torch.rand(M, generator=gen) * 0.05 + 0.001, (torch.rand(N, generator=gen) + 0.5) * 0.02 / max(K, 1) ** 0.5
+    b = torch.randn(N, generator=gen).to(TYPES[out]) if bias else None
+    return x, sx, w, sw, b
+
+
+def check(Y, x, sx, w, sw, b):
+    """Y (GPU) of CPU operands; float64 holds every sum exactly."""
+    acc = x.double() @ w.double().t()
+    scaled = acc * sx.double()[:, None] * sw.double()
+    ref = scaled if b is None else scaled + b.double()
+    t = Y.dtype
+    half = 0 if t == torch.float32 else torch.finfo(t).eps / 2
+    bound = scaled.abs() * 3 * 2.0 ** -24 + ref.abs() * (half + 2.0 ** -24) + torch.finfo(t).tiny * torch.finfo(t).eps
+    # past the type's largest value the output is infinite: all that lies beyond counts as that value
+    most = torch.finfo(t).max
+    off = (Y.cpu().double().clamp(-most, most) - ref.clamp(-most, most)).abs()
+    assert bool((off <= bound * (1 + 1e-9)).all()), (off - bound).max()
+
+
+def run(M, N, K, out="bf16", bias=False, seed=0):
+    x, sx, w, sw, b = operands(M, N, K, out, bias, seed)
+    dev = [t.cuda() if t is not None else None for t in (x, sx, w, sw, b)]
+    Y = i8.i8_matmul(*dev[:4], bias=dev[4], out=torch.full((M, N), float("nan"), dtype=TYPES[out], device="cuda"))
+    check(Y, x, sx, w, sw, b)
+
+
+@pytest.mark.parametrize("M", [1, 2, 4, 5, 15, 16, 17, 31, 32, 33, 48, 63, 64])
+@pytest.mark.parametrize("N, K", [(1, 16), (16, 16), (15, 64), (33, 48), (64, 256), (100, 272), (250, 1040), (4112, 1024),
+                                  (5000, 2064), (96, 8192)])
+def test_few_rows(M, N, K):
+    print("few", M, N, K, flush=True)
+    out = list(TYPES)[(M + N + K) % 3]
+    run(M, N, K, out, bias=M % 2 == 0)
+
+
+@pytest.mark.parametrize("M, N, K", [(65, 64, 16), (65, 1, 128), (100, 100, 96), (128, 128, 4096), (200, 3000, 320), (257, 511, 1040),
+                                     (1000, 777, 2064), (4096, 300, 64), (300, 5000, 512), (1024, 1024, 1024), (2049, 2111, 160),
+                                     (520, 12000, 272), (4000, 4100, 144)])
+@pytest.mark.parametrize("out", TYPES)
+def test_tiles(M, N, K, out):
+    print("tiles", M, N, K, out, flush=True)
+    run(M, N, K, out, bias=True)
+    run(M, N, K, out, bias=False, seed=5)
+
+
+def test_every_kernel_runs():
+    """Sizes at which the planner takes each compiled kernel, edges cut."""
+    found = {}
+    for M in [1, 3, 9, 16, 30, 50, 64, 65] + list(range(101, 5000, 180)):
+        for N in [20, 1003, 5003] + list(range(101, 9000, 170)):
+            p = g.gemm_i8_problem()
+            p.M, p.N, p.K, p.sx, p.sw, p.sy, p.out = M, N, 160, 160, 160, N, g.GEMM_BF16
+            found.setdefault(i8.gemm_i8_plan_create(p).describe().split()[0], (M, N))
+    assert len(found) >= 8
+    for kernel, (M, N) in found.items():
+        print(kernel, M, N, flush=True)
+        run(M, N, 160, bias=True)
+        run(M, N, 1040, out="f32")
+
+
+@pytest.mark.parametrize("M, N, K", [(1, 1, 1), (3, 5, 7), (16, 16, 15), (64, 64, 17), (65, 63, 127), (1, 300, 129), (70, 70, 1000),
+                                     (200, 130, 2005), (777, 1003, 1999), (64, 64, 33)])
+def test_any_sizes(M, N, K):
+    print("any", M, N, K, flush=True)
+    for i, out in enumerate(TYPES):
+        run(M, N, K, out, bias=i != 1)
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_views(M):
+    """Rows at any address and distance, rows that share memory, outputs apart from each other."""
+    N, K = 150, 256
+    big_x, big_w = int8((M, 2 * K + 31), 1).cuda(), int8((N, 2 * K + 32), 2).cuda()
+    sx, sw = torch.rand(M, device="cuda"), torch.rand(N + 3, device="cuda")[3:]
+    for x, w in [(big_x[:, 1:1 + K], big_w[:, 16:16 + K]), (big_x[:, 16:16 + K], big_w[:, 16:16 + K]),
+                 (big_x[:, :K], big_w[:, 7:7 + K]), (big_x[:, :K - 3], big_w[:, 2:K - 1]),
+                 (big_x[:1, :K].expand(M, K), big_w[:, :K]), (big_x[:, :K].contiguous(), big_w[:1, 32:32 + K].expand(N, K)),
+                 (big_x[:1, :K].contiguous().expand(M, K), big_w[:, :K].contiguous()),
+                 (big_w[: min(M, N), :K], big_w[:, :K])]:
+        m = x.shape[0]
+        wide = torch.full((m, N + 5), float("nan"), dtype=torch.float16, device="cuda")
+        Y = i8.i8_matmul(x, sx[:m], w, sw, out=wide[:, 2:2 + N])
+        check(Y, x.cpu(), sx[:m].cpu(), w.cpu(), sw.cpu(), None)
+        assert bool(torch.isnan(wide[:, :2]).all()) and bool(torch.isnan(wide[:, 2 + N:]).all())
+
+
+def test_values_at_the_ends():
+    """Sums at int32's edge: K below 2^17 products of 128 x 128."""
+    for M, N, K in ((2, 40, (1 << 17) - 16), (70, 20, (1 << 17) - 16), (3, 3, (1 << 17) - 1)):
+        x, w = torch.full((M, K), -128, dtype=torch.int8), torch.full((N, K), -128, dtype=torch.int8)
+        w[1] = 127
+        sx, sw = torch.full((M,), 0.5), torch.full((N,), 2.0 ** -20)
+        Y = i8.i8_matmul(x.cuda(), sx.cuda(), w.cuda(), sw.cuda(), out_dtype=torch.float32)
+        check(Y, x, sx, w, sw, None)
+    # scales of zero, infinity and NaN stay in their rows and columns
+    x, sx, w, sw, b = operands(70, 90, 256, "bf16", True, 1)
+    sx[3], sx[5], sw[7] = 0.0, float("nan"), float("nan")
+    for m in (10, 70):
+        Y = i8.i8_matmul(x[:m].cuda(), sx[:m].cuda(), w.cuda(), sw.cuda(), bias=b.cuda()).cpu()
+        rows = [r for r in range(m) if r != 5]
+        cols = [c for c in range(90) if c != 7]
+        assert bool(torch.isnan(Y[5]).all()) and bool(torch.isnan(Y[:, 7]).all())
+        check(Y[rows][:, cols].cuda(), x[rows], sx[rows], w[cols], sw[cols], b[cols])
+        assert torch.equal(Y[3][cols], b[cols])
+
+
+def test_nothing_to_sum_and_nothing_to_write():
+    b = torch.randn(9, device="cuda").half()
+    e = torch.empty(4, 0, dtype=torch.int8, device="cuda"), torch.ones(4, device="cuda")
+    f = torch.empty(9, 0, dtype=torch.int8, device="cuda"), torch.ones(9, device="cuda")
+    assert torch.equal(i8.i8_matmul(*e, *f, bias=b, out_dtype=torch.float16), b.expand(4, 9))
+    assert torch.equal(i8.i8_matmul(*e, *f), torch.zeros(4, 9, dtype=torch.bfloat16, device="cuda"))
+    x = torch.empty(0, 32, dtype=torch.int8, device="cuda"), torch.empty(0, device="cuda")
+    w = torch.zeros(5, 32, dtype=torch.int8, device="cuda"), torch.ones(5, device="cuda")
+    assert i8.i8_matmul(*x, *w).shape == (0, 5) and i8.i8_matmul(*w, *x).shape == (5, 0)
+
+
+def test_quantized_rows_make_the_product():
+    """What a user does: weights once, activations before the product."""
+    gen = torch.Generator().manual_seed(1)
+    X, W = torch.randn(33, 640, generator=gen).bfloat16(), (torch.randn(200, 640, generator=gen) / 25).bfloat16()
+    x, w = i8.i8_quantize(X.cuda()), i8.i8_quantize(W.cuda())
+    Y = i8.i8_matmul(*x, *w)
+    check(Y, *(t.cpu() for t in x + w), None)
+    # half a step of each operand on each of 640 terms, as a random walk: about 0.8 % of the result
+    ref = X.double() @ W.double().t()
+    assert float((Y.cpu().double() - ref).norm() / ref.norm()) < 0.02
+
+
+def test_streams_and_graphs():
+    x, sx, w, sw, b = (t.cuda() for t in operands(24, 1024, 1024, "bf16", True, 1))
+    want = i8.i8_matmul(x, sx, w, sw, bias=b)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = i8.i8_matmul(x, sx, w, sw, bias=b, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
+    many = int8((700, 1024), 9).cuda(), torch.rand(700, device="cuda")
+    step = lambda: [i8.i8_matmul(x, sx, w, sw, bias=b), i8.i8_matmul(*many, w, sw), i8.i8_matmul(many[0][:, 1:], many[1], w[:, 1:], sw)]
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for i in range(3):
+        x.copy_(int8((24, 1024), 20 + i))
+        many[0].copy_(int8((700, 1024), 30 + i))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in captured]
+        for a, c in zip(got, step()):
+            assert torch.equal(a, c)
