@@ -1,18 +1,26 @@
-// Native side of the torch calls that grouped.py and w4.py have already checked
-// once: from the arguments' types, shapes, strides and devices to the plan and
-// the launch, without Python in between.  A decode-sized product is bound by
-// its host time: 4.1 to 4.9 us here, 3.4 of them the library's call, against 7.4
-// where the call is checked (out given) and passed on by ctypes.
+// Native side of the torch calls that grouped.py, w4.py, i8.py, norm.py and
+// router.py have already checked once: from the arguments' types, shapes, strides
+// and devices to the plan and the launch, without Python in between.  A
+// decode-sized product is bound by its host time: 4.1 to 4.9 us here, 3.4 of them
+// the library's call, against 7.4 where the call is checked (out given) and passed
+// on by ctypes.
 //
 //   remember(kind, owner, plan, run, workspace, sizes, dtype, extra, tensors)
 //       a call that passed the checks: its gemm_*_run address, plan handle (kept
 //       alive by `owner`), workspace bytes, output sizes and type.  `extra`: the
-//       call's other argument (an int, a dtype or None).
+//       call's other arguments (an int, a float, a dtype, None, or a tuple of these).
+//       The row operators (norm, int8 rows, routing) have no plan: that the checks
+//       were passed is all there is to remember.
 //   call(kind, extra, *tensors)
 //       the outputs; None for a call not remembered (or on a device that is not
 //       the current one): the caller then takes the checked path; a non-zero
 //       gemm_status as an int if the library refused.
 //   forget()
+//   norm(x, weight, residual, eps), norm_i8(...), i8_rows(X), route(logits, bias, parameters)
+//       these operators on arguments that have been checked, with their gradients
+//       (one Function each, which records itself where a gradient is needed)
+//   functions(addresses)
+//       where the library's entry points are, in the order of `Library`
 //
 // Only plain torch.Tensor and Parameter objects on a GPU are looked up.  The
 // interpreter's lock guards the table; it is released for the allocations and
@@ -21,15 +29,20 @@
 #include <ATen/ATen.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstring>
 #include <unordered_map>
 #include <utility>
 
+#include "../../include/gemm.h"
+
 namespace {
 
-enum Kind { kMatmul = 0, kWgrad = 1, kRows = 2, kW4 = 3, kKinds };
+enum Kind { kMatmul = 0, kWgrad, kRows, kW4, kNorm, kNormI8, kI8Rows, kI8, kRoute, kKinds };
+bool has_plan(int kind) { return kind <= kW4 || kind == kI8; }
 constexpr int kMaxWords = 64;
 constexpr size_t kMostCalls = 4096;
 
@@ -97,6 +110,18 @@ bool push_tensor(Key* k, PyObject* o, int* device) {
 
 // `extra`: dtypes and None are singletons, known by address.
 bool push_extra(Key* k, PyObject* o) {
+    if (PyTuple_CheckExact(o)) {
+        if (!k->push(4) || !k->push(PyTuple_GET_SIZE(o))) return false;
+        for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(o); ++i)
+            if (PyTuple_CheckExact(PyTuple_GET_ITEM(o, i)) || !push_extra(k, PyTuple_GET_ITEM(o, i))) return false;
+        return true;
+    }
+    if (PyFloat_CheckExact(o)) {
+        const double v = PyFloat_AS_DOUBLE(o);
+        int64_t bits;
+        std::memcpy(&bits, &v, sizeof bits);
+        return k->push(3) && k->push(bits);
+    }
     if (PyLong_CheckExact(o)) {
         const int64_t v = PyLong_AsLongLong(o);
         if (v == -1 && PyErr_Occurred()) {
@@ -147,7 +172,10 @@ Result launch(int kind, const Entry& e, const at::Tensor& like, const void* cons
         return r;
     }
     r.out = make(at::IntArrayRef(e.sizes, e.dims), e.dtype, like);
-    if (kind == kW4) {
+    if (kind == kI8) {
+        typedef int (*fn)(void*, const void*, const void*, const void*, const void*, const void*, void*, void*);
+        r.status = reinterpret_cast<fn>(e.run)(e.plan, in[0], in[1], in[2], in[3], in[4], r.out.data_ptr(), stream);
+    } else if (kind == kW4) {
         typedef int (*fn)(void*, const void*, const void*, const void*, const void*, const void*, void*, void*);
         r.status = reinterpret_cast<fn>(e.run)(e.plan, in[0], in[1], in[2], in[3], in[4], r.out.data_ptr(), stream);
     } else {
@@ -160,7 +188,311 @@ Result launch(int kind, const Entry& e, const at::Tensor& like, const void* cons
 }
 
 constexpr int kMostOperands = 5;
-int operands(int kind) { return kind == kRows ? 1 : kind == kW4 ? 5 : 3; }
+int operands(int kind) {
+    switch (kind) {
+        case kRows:
+        case kI8Rows: return 1;
+        case kRoute: return 2;
+        case kW4:
+        case kI8: return 5;
+        default: return 3;
+    }
+}
+
+// ---------------------------------------------------------------- the row operators
+
+struct Library {
+    gemm_status (*norm)(const gemm_norm_problem*, const void*, const void*, const void*, void*, void*, float*, void*);
+    gemm_status (*norm_i8)(const gemm_norm_problem*, const void*, const void*, const void*, void*, int8_t*, float*, void*);
+    gemm_status (*norm_grad_workspace)(const gemm_norm_problem*, size_t*);
+    gemm_status (*norm_grad)(const gemm_norm_problem*, const void*, const void*, const void*, const void*, const float*, void*,
+                             void*, void*, size_t, void*);
+    gemm_status (*quantize)(const void*, gemm_dtype, int64_t, int64_t, int64_t, int8_t*, int64_t, float*, void*);
+    gemm_status (*route)(const gemm_route_problem*, const void*, const float*, float*, int32_t*, void*);
+    gemm_status (*route_grad)(const gemm_route_problem*, const void*, const int32_t*, const float*, void*, void*);
+    const char* (*last_error)();
+};
+Library library;
+
+struct Refused {   // by the library, with this status
+    int status;
+};
+void check(gemm_status st) {
+    if (st != GEMM_OK) throw Refused{static_cast<int>(st)};
+}
+// In a backward pass there is no Python to hand a status to.
+void check_backward(gemm_status st) {
+    if (st != GEMM_OK) throw std::runtime_error(library.last_error());
+}
+
+using torch::autograd::AutogradContext;
+using torch::autograd::variable_list;
+
+gemm_dtype code(const at::Tensor& t) {
+    return t.scalar_type() == at::kHalf ? GEMM_F16 : t.scalar_type() == at::kBFloat16 ? GEMM_BF16 : GEMM_F32;
+}
+void* stream_of(const at::Tensor& t) { return c10::hip::getCurrentHIPStream(t.device().index()).stream(); }
+void* data(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+
+// A gradient whose rows are contiguous (a sum's is expanded from one value).
+at::Tensor as_rows(const at::Tensor& t) {
+    return !t.defined() || t.size(1) <= 1 || t.stride(1) == 1 ? t : t.contiguous();
+}
+
+// These gradients have none of their own: whoever differentiates them is told.
+variable_list once(variable_list grads, const char* what) {
+    if (!at::GradMode::is_enabled()) return grads;
+    for (auto& g : grads)
+        if (g.defined()) g = g.detach().set_requires_grad(true);
+    auto error = std::make_shared<torch::autograd::DelayedError>(std::string("the gradient of ") + what + " is not differentiable",
+                                                                 static_cast<int64_t>(grads.size()));
+    return (*error)(std::move(grads));
+}
+
+gemm_norm_problem norm_problem(const at::Tensor& x, const at::Tensor& w, const at::Tensor& r, double eps, int64_t sy) {
+    gemm_norm_problem p = {};
+    p.R = x.size(0);
+    p.K = x.size(1);
+    p.sx = x.stride(0);
+    p.sy = sy;
+    if (r.defined()) {
+        p.sr = r.stride(0);
+        p.sh = p.K;
+        p.has_residual = 1;
+    }
+    p.dtype = code(x);
+    p.weight = code(w);
+    p.eps = static_cast<float>(eps);
+    return p;
+}
+
+// y (into), h where there is a residual, rstd where it is wanted
+struct Normed {
+    at::Tensor y, h, rstd;
+};
+Normed norm_rows(const at::Tensor& x, const at::Tensor& w, const at::Tensor& r, double eps, bool want_rstd) {
+    Normed n;
+    n.y = make({x.size(0), x.size(1)}, x.scalar_type(), x);
+    if (r.defined()) n.h = make({x.size(0), x.size(1)}, x.scalar_type(), x);
+    if (want_rstd) n.rstd = make({x.size(0)}, at::kFloat, x);
+    const gemm_norm_problem p = norm_problem(x, w, r, eps, x.size(1));
+    check(library.norm(&p, data(x), data(r), data(w), data(n.h), data(n.y), static_cast<float*>(data(n.rstd)), stream_of(x)));
+    return n;
+}
+
+struct NormFunction : torch::autograd::Function<NormFunction> {
+    static variable_list forward(AutogradContext* ctx, const at::Tensor& x, const at::Tensor& w, const std::optional<at::Tensor>& r,
+                                 double eps) {
+        const Normed n = norm_rows(x, w, r ? *r : at::Tensor(), eps, true);
+        ctx->set_materialize_grads(false);
+        ctx->save_for_backward({n.h.defined() ? n.h : x, w, n.rstd});
+        if (n.h.defined()) return {n.y, n.h};
+        return {n.y};
+    }
+
+    static variable_list backward(AutogradContext* ctx, variable_list grads) {
+        const auto saved = ctx->get_saved_variables();
+        const at::Tensor &h = saved[0], &w = saved[1], &rstd = saved[2];
+        const at::Tensor dy = as_rows(grads[0]), dh = grads.size() > 1 ? as_rows(grads[1]) : at::Tensor();
+        const c10::DeviceGuard guard(h.device());
+        at::Tensor dx = dh, dw;
+        if (dy.defined()) {
+            dx = make({h.size(0), h.size(1)}, h.scalar_type(), h);
+            gemm_norm_problem p = norm_problem(dx, w, dh, 1.0, dy.stride(0));
+            p.sh = h.stride(0);
+            at::Tensor ws;
+            size_t need = 0;
+            if (ctx->needs_input_grad(1)) {
+                dw = make({w.size(0)}, w.scalar_type(), w);
+                check_backward(library.norm_grad_workspace(&p, &need));
+                if (need > 0) ws = make({static_cast<int64_t>(need)}, at::kByte, h);
+            }
+            check_backward(library.norm_grad(&p, data(dy), data(dh), data(h), data(w), static_cast<const float*>(data(rstd)), data(dx),
+                                             data(dw), data(ws), need, stream_of(h)));
+        }
+        const bool residual = grads.size() > 1;
+        return once({ctx->needs_input_grad(0) ? dx : at::Tensor(), dw,
+                     residual && ctx->needs_input_grad(2) ? dx : at::Tensor(), at::Tensor()}, "rms_norm");
+    }
+};
+
+bool wants_grad(const at::Tensor& t) { return t.defined() && t.requires_grad(); }
+
+// The outputs of an operator, in order.
+variable_list norm_call(const at::Tensor& x, const at::Tensor& w, const at::Tensor& r, double eps) {
+    if (at::GradMode::is_enabled() && (wants_grad(x) || wants_grad(w) || wants_grad(r)))
+        return NormFunction::apply(x, w, r.defined() ? std::optional<at::Tensor>(r) : std::nullopt, eps);
+    const Normed n = norm_rows(x, w, r, eps, false);
+    if (n.h.defined()) return {n.y, n.h};
+    return {n.y};
+}
+
+variable_list norm_i8_call(const at::Tensor& x, const at::Tensor& w, const at::Tensor& r, double eps) {
+    at::Tensor q = make({x.size(0), x.size(1)}, at::kChar, x), scale = make({x.size(0)}, at::kFloat, x), h;
+    if (r.defined()) h = make({x.size(0), x.size(1)}, x.scalar_type(), x);
+    const gemm_norm_problem p = norm_problem(x, w, r, eps, x.size(1));
+    check(library.norm_i8(&p, data(x), data(r), data(w), data(h), static_cast<int8_t*>(data(q)), static_cast<float*>(data(scale)),
+                          stream_of(x)));
+    if (h.defined()) return {q, scale, h};
+    return {q, scale};
+}
+
+variable_list i8_rows_call(const at::Tensor& x) {
+    at::Tensor q = make({x.size(0), x.size(1)}, at::kChar, x), scale = make({x.size(0)}, at::kFloat, x);
+    check(library.quantize(data(x), code(x), x.size(0), x.size(1), x.stride(0), static_cast<int8_t*>(data(q)), x.size(1),
+                           static_cast<float*>(data(scale)), stream_of(x)));
+    return {q, scale};
+}
+
+// The parameters of a routing: top, score, groups, top_groups, group_best, renormalize, scale.
+constexpr int kRouteInts = 6;
+struct RouteParameters {
+    int64_t v[kRouteInts];
+    double scale;
+};
+
+gemm_route_problem route_problem(const at::Tensor& logits, bool bias, const RouteParameters& a) {
+    gemm_route_problem p = {};
+    p.R = logits.size(0);
+    p.E = static_cast<int32_t>(logits.size(1));
+    p.sl = logits.stride(0);
+    p.top = static_cast<int32_t>(a.v[0]);
+    p.score = static_cast<gemm_score>(a.v[1]);
+    p.groups = static_cast<int32_t>(a.v[2]);
+    p.top_groups = static_cast<int32_t>(a.v[3]);
+    p.group_best = static_cast<int32_t>(a.v[4]);
+    p.renormalize = static_cast<int32_t>(a.v[5]);
+    p.has_bias = bias ? 1 : 0;
+    p.scale = static_cast<float>(a.scale);
+    p.dtype = code(logits);
+    return p;
+}
+
+variable_list route_rows(const at::Tensor& logits, const at::Tensor& bias, const RouteParameters& a) {
+    at::Tensor w = make({logits.size(0), a.v[0]}, at::kFloat, logits), ids = make({logits.size(0), a.v[0]}, at::kInt, logits);
+    const gemm_route_problem p = route_problem(logits, bias.defined(), a);
+    check(library.route(&p, data(logits), static_cast<const float*>(data(bias)), static_cast<float*>(data(w)),
+                        static_cast<int32_t*>(data(ids)), stream_of(logits)));
+    return {w, ids};
+}
+
+struct RouteFunction : torch::autograd::Function<RouteFunction> {
+    static variable_list forward(AutogradContext* ctx, const at::Tensor& logits, const std::optional<at::Tensor>& bias,
+                                 const std::vector<int64_t>& v, double scale) {
+        RouteParameters a;
+        std::copy(v.begin(), v.end(), a.v);
+        a.scale = scale;
+        variable_list out = route_rows(logits, bias ? *bias : at::Tensor(), a);
+        ctx->set_materialize_grads(false);
+        ctx->mark_non_differentiable({out[1]});
+        ctx->save_for_backward({logits, out[1]});
+        ctx->saved_data["v"] = v;
+        ctx->saved_data["scale"] = scale;
+        return out;
+    }
+
+    static variable_list backward(AutogradContext* ctx, variable_list grads) {
+        if (!grads[0].defined()) return {at::Tensor(), at::Tensor(), at::Tensor(), at::Tensor()};
+        const auto saved = ctx->get_saved_variables();
+        const at::Tensor &logits = saved[0], &ids = saved[1];
+        const auto v = ctx->saved_data["v"].toIntVector();
+        RouteParameters a;
+        std::copy(v.begin(), v.end(), a.v);
+        a.scale = ctx->saved_data["scale"].toDouble();
+        const c10::DeviceGuard guard(logits.device());
+        const at::Tensor dw = grads[0].contiguous();
+        at::Tensor dl = make({logits.size(0), logits.size(1)}, logits.scalar_type(), logits);
+        const gemm_route_problem p = route_problem(logits, false, a);
+        check_backward(library.route_grad(&p, data(logits), static_cast<const int32_t*>(data(ids)), static_cast<const float*>(data(dw)),
+                                          data(dl), stream_of(logits)));
+        return once({dl, at::Tensor(), at::Tensor(), at::Tensor()}, "route");
+    }
+};
+
+variable_list route_call(const at::Tensor& logits, const at::Tensor& bias, const RouteParameters& a) {
+    if (at::GradMode::is_enabled() && wants_grad(logits))
+        return RouteFunction::apply(logits, bias.defined() ? std::optional<at::Tensor>(bias) : std::nullopt,
+                                    std::vector<int64_t>(a.v, a.v + kRouteInts), a.scale);
+    return route_rows(logits, bias, a);
+}
+
+at::Tensor tensor_or_none(PyObject* o) { return o == Py_None ? at::Tensor() : THPVariable_Unpack(o); }
+
+bool route_parameters(PyObject* o, RouteParameters* a) {
+    if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != kRouteInts + 1) {
+        PyErr_SetString(PyExc_TypeError, "route: seven parameters");
+        return false;
+    }
+    for (int i = 0; i < kRouteInts; ++i) {
+        a->v[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(o, i));
+        if (a->v[i] == -1 && PyErr_Occurred()) return false;
+        if (a->v[i] != static_cast<int32_t>(a->v[i])) a->v[i] = -1;   // no 32-bit value: refused as negative ones are
+    }
+    a->scale = PyFloat_AsDouble(PyTuple_GET_ITEM(o, kRouteInts));
+    return !(a->scale == -1.0 && PyErr_Occurred());
+}
+
+// One of these on checked arguments: a tensor, a tuple of them, or the library's
+// status as an int.
+PyObject* row_operator(int kind, PyObject* extra, PyObject* const* t) {
+    variable_list out;
+    RouteParameters a;
+    double eps = 0.0;
+    if (kind == kRoute && !route_parameters(extra, &a)) return nullptr;
+    if (kind == kNorm || kind == kNormI8) {
+        eps = PyFloat_AsDouble(extra);
+        if (eps == -1.0 && PyErr_Occurred()) return nullptr;
+    }
+    at::Tensor in[3];
+    for (int i = 0; i < operands(kind); ++i) in[i] = tensor_or_none(t[i]);
+    try {
+        const Unlocked unlocked;
+        out = kind == kNorm     ? norm_call(in[0], in[1], in[2], eps)
+              : kind == kNormI8 ? norm_i8_call(in[0], in[1], in[2], eps)
+              : kind == kI8Rows ? i8_rows_call(in[0])
+                                : route_call(in[0], in[1], a);
+    } catch (const Refused& r) {
+        return PyLong_FromLong(r.status);
+    }
+    if (out.size() == 1) return THPVariable_Wrap(std::move(out[0]));
+    PyObject* tuple = PyTuple_New(static_cast<Py_ssize_t>(out.size()));
+    for (size_t i = 0; i < out.size(); ++i) PyTuple_SET_ITEM(tuple, static_cast<Py_ssize_t>(i), THPVariable_Wrap(std::move(out[i])));
+    return tuple;
+}
+
+// The same from Python: norm(x, weight, residual, eps) and its like.
+template <int KIND>
+PyObject* py_row_operator(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    const int tensors = operands(KIND);
+    bool fits = n == tensors + (KIND == kI8Rows ? 0 : 1);
+    for (int i = 0; fits && i < tensors; ++i)
+        fits = (args[i] == Py_None && i > 0) || (THPVariable_Check(args[i]) && THPVariable_Unpack(args[i]).is_cuda());
+    if (!fits) {
+        PyErr_SetString(PyExc_TypeError, "checked GPU tensors, and the operator's parameters");
+        return nullptr;
+    }
+    try {
+        return row_operator(KIND, n > tensors ? args[tensors] : Py_None, args);
+    } catch (const std::exception& ex) {
+        PyErr_SetString(PyExc_RuntimeError, ex.what());
+        return nullptr;
+    }
+}
+
+PyObject* py_functions(PyObject*, PyObject* args) {
+    constexpr int count = sizeof(Library) / sizeof(void*);
+    if (PyTuple_GET_SIZE(args) != count) {
+        PyErr_SetString(PyExc_TypeError, "functions: as many addresses as entry points");
+        return nullptr;
+    }
+    void* at[count];
+    for (int i = 0; i < count; ++i) {
+        at[i] = reinterpret_cast<void*>(static_cast<uintptr_t>(PyLong_AsUnsignedLongLong(PyTuple_GET_ITEM(args, i))));
+        if (PyErr_Occurred()) return nullptr;
+    }
+    std::memcpy(&library, at, sizeof library);
+    Py_RETURN_NONE;
+}
 
 bool read_key(Key* key, PyObject* extra, PyObject* const* t, int n, int* device) {
     *device = -1;
@@ -183,6 +515,7 @@ PyObject* py_call(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const auto& calls = table(kind);
         const auto hit = calls.find(key);
         if (hit == calls.end() || c10::hip::current_device() != hit->second.device) Py_RETURN_NONE;
+        if (!has_plan(static_cast<int>(kind))) return row_operator(static_cast<int>(kind), args[1], args + 2);
         const Entry e = hit->second;   // the table may change while the lock is released
         const Held plan(e.owner);
         const at::Tensor like = THPVariable_Unpack(args[2]);
@@ -253,6 +586,13 @@ PyMethodDef methods[] = {
     {"call", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(py_call)), METH_FASTCALL, nullptr},
     {"remember", py_remember, METH_VARARGS, nullptr},
     {"forget", py_forget, METH_NOARGS, nullptr},
+    {"functions", py_functions, METH_VARARGS, nullptr},
+#define DTG_ROW(NAME, KIND) \
+    {NAME, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(&py_row_operator<KIND>)), METH_FASTCALL, nullptr}
+    DTG_ROW("norm", kNorm),
+    DTG_ROW("norm_i8", kNormI8),
+    DTG_ROW("i8_rows", kI8Rows),
+    DTG_ROW("route", kRoute),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -104,24 +104,49 @@ _lock = threading.Lock()   # guards _plans
 # remembered by _binding.so, by what the checks look at: the operands' types,
 # shapes, strides and devices.  A call found there goes straight to the launch:
 # 4.1 to 4.9 us of host time instead of 7.4, which is what the smallest products take.
-MATMUL, WGRAD, ROWS, W4 = range(4)   # csrc/binding.cpp
+MATMUL, WGRAD, ROWS, W4, NORM, NORM_I8, I8_ROWS, I8, ROUTE = range(9)   # csrc/binding.cpp
 _call = None
 _raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _address(name):
+    return ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value
 
 
 def _remembered(kind, extra, *tensors):
     """The call's outputs, or None where it has to be checked first."""
     global _call
     if _call is None:
-        _call = binding().call
+        _call = _native().call
     r = _call(kind, extra, *tensors)
     if type(r) is int:
         _check(r)
     return r
 
 
-def _address(name):
-    return ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value
+_bound = None
+
+
+def _native():
+    """_binding.so, which knows where libgemm.so's row operators are."""
+    global _bound
+    if _bound is None:
+        b = binding()
+        b.functions(*[_address(name) for name in (
+            "gemm_rms_norm", "gemm_rms_norm_i8", "gemm_rms_norm_grad_workspace", "gemm_rms_norm_grad", "gemm_i8_quantize",
+            "gemm_route", "gemm_route_grad", "gemm_last_error")])
+        _bound = b
+    return _bound
+
+
+def _row_operator(name, kind, remember, extra, *tensors):
+    """A row operator of _binding.so on checked arguments; `remember`: such calls go there at once from now on."""
+    r = getattr(_native(), name)(*tensors, *(() if extra is None else (extra,)))
+    if type(r) is int:
+        _check(r)
+    if remember:
+        binding().remember(kind, None, 0, 0, 0, (), torch.uint8, extra, tensors)
+    return r
 
 
 def _remember(kind, plan, run, workspace, sizes, dtype, extra, *tensors):

@@ -13,7 +13,7 @@ import threading
 import torch
 
 from . import GEMM_BF16, GEMM_F16, GEMM_F32, _check, _keep_plan, _p, gemm_i8_problem, lib
-from .grouped import _need_gpu, _on_stream, _raw_stream
+from .grouped import I8, I8_ROWS, _need_gpu, _on_stream, _raw_stream, _remember, _remembered, _row_operator
 from .norm import _rows_arg
 
 _CODES = {torch.float16: GEMM_F16, torch.bfloat16: GEMM_BF16, torch.float32: GEMM_F32}
@@ -72,17 +72,13 @@ def i8_quantize(X, stream=None):
     weight (N x K) with one per channel.  A row of zeros has the scale 0, a row
     with an infinity or a NaN the scale NaN.  No gradients.  Asynchronous on
     `stream` (default: torch's current stream)."""
+    if stream is None:
+        pair = _remembered(I8_ROWS, None, X)
+        if pair is not None:
+            return pair
     _rows_arg("X", X)
     _need_gpu(X.device, ("X", X))
-
-    def call():
-        R, K = X.shape
-        q = torch.empty((R, K), dtype=torch.int8, device=X.device)
-        scale = torch.empty(R, dtype=torch.float32, device=X.device)
-        gemm_i8_quantize(X.data_ptr(), _CODES[X.dtype], R, K, X.stride(0), q.data_ptr(), K, scale.data_ptr(),
-                         _raw_stream(X.device.index))
-        return q, scale
-    return _on_stream(call, X.device, stream, (X,))
+    return _on_stream(lambda: _row_operator("i8_rows", I8_ROWS, stream is None, None, X), X.device, stream, (X,))
 
 
 def _vector_arg(name, t, n, dtype):
@@ -101,6 +97,11 @@ def i8_matmul(X, x_scale, W, w_scale, bias=None, out_dtype=torch.bfloat16, out=N
     sums are exact; the scales and the bias are applied in float32, with one
     rounding to the output's type.  No gradients.  Asynchronous on `stream`
     (default: torch's current stream)."""
+    plain = out is None and stream is None
+    if plain:
+        Y = _remembered(I8, out_dtype, X, x_scale, W, w_scale, bias)
+        if Y is not None:
+            return Y
     dtype = out_dtype if out is None else out.dtype
     if X.dtype != torch.int8 or W.dtype != torch.int8:
         raise TypeError("X and W must be int8, got %s and %s" % (X.dtype, W.dtype))
@@ -135,5 +136,7 @@ def i8_matmul(X, x_scale, W, w_scale, bias=None, out_dtype=torch.bfloat16, out=N
                     plan = _keep_plan(_plans, key, gemm_i8_plan_create(p, X.device.index))
         gemm_i8_run(plan, X.data_ptr(), x_scale.data_ptr(), W.data_ptr(), w_scale.data_ptr(),
                     bias.data_ptr() if bias is not None else None, Y.data_ptr(), _raw_stream(X.device.index))
+        if plain:
+            _remember(I8, plan, "gemm_i8_run", 0, (M, N), dtype, out_dtype, X, x_scale, W, w_scale, bias)
         return Y
     return _on_stream(call, X.device, stream, (X, x_scale, W, w_scale, bias, out))

@@ -12,7 +12,7 @@ import ctypes
 import torch
 
 from . import GEMM_BF16, GEMM_F16, GEMM_F32, _check, gemm_norm_problem, lib
-from .grouped import _need_gpu, _on_stream, _raw_stream
+from .grouped import NORM, NORM_I8, _need_gpu, _on_stream, _raw_stream, _remembered, _row_operator
 
 _CODES = {torch.float16: GEMM_F16, torch.bfloat16: GEMM_BF16, torch.float32: GEMM_F32}
 
@@ -67,28 +67,8 @@ def _arguments(x, weight, residual):
     _need_gpu(x.device, ("x", x), ("weight", weight), ("residual", residual))
 
 
-def _problem(x, weight, residual, eps, out):
-    p = gemm_norm_problem()
-    p.R, p.K = x.shape
-    p.sx, p.sy = x.stride(0), out.stride(0)
-    if residual is not None:
-        p.sr, p.sh, p.has_residual = residual.stride(0), x.shape[1], 1
-    p.dtype, p.weight, p.eps = _CODES[x.dtype], _CODES[weight.dtype], eps
-    return p
-
-
 def _address(t):
     return t.data_ptr() if t is not None else None
-
-
-def _forward(x, weight, residual, eps, want_rstd):
-    R, K = x.shape
-    y = torch.empty((R, K), dtype=x.dtype, device=x.device)
-    h = torch.empty_like(y) if residual is not None else None
-    rstd = torch.empty(R, dtype=torch.float32, device=x.device) if want_rstd else None
-    gemm_rms_norm(_problem(x, weight, residual, eps, y), x.data_ptr(), _address(residual), weight.data_ptr(), _address(h),
-                  y.data_ptr(), _address(rstd), _raw_stream(x.device.index))
-    return y, h, rstd
 
 
 def rms_norm_grad(dy, h, weight, rstd, dh=None, need_weight=True):
@@ -107,8 +87,12 @@ def rms_norm_grad(dy, h, weight, rstd, dh=None, need_weight=True):
 
     def call():
         dx = torch.empty(h.shape, dtype=h.dtype, device=h.device)
-        p = _problem(dx, weight, dh, 1.0, dy)
-        p.sh = h.stride(0)
+        p = gemm_norm_problem()
+        p.R, p.K = h.shape
+        p.sx, p.sy, p.sh = dx.stride(0), dy.stride(0), h.stride(0)
+        if dh is not None:
+            p.sr, p.has_residual = dh.stride(0), 1
+        p.dtype, p.weight, p.eps = _CODES[h.dtype], _CODES[weight.dtype], 1.0   # eps is in rstd
         dw, ws, need = None, None, 0
         if need_weight:
             dw = torch.empty(weight.shape, dtype=weight.dtype, device=h.device)
@@ -120,30 +104,6 @@ def rms_norm_grad(dy, h, weight, rstd, dh=None, need_weight=True):
     return _on_stream(call, h.device, None, ())
 
 
-def _as_rows(grad):
-    """A gradient whose rows are contiguous (a sum's is expanded from one value)."""
-    return grad if grad is None or grad.shape[1] <= 1 or grad.stride(1) == 1 else grad.contiguous()
-
-
-class _RmsNorm(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, weight, residual, eps):
-        y, h, rstd = _forward(x, weight, residual, eps, True)
-        ctx.set_materialize_grads(False)
-        ctx.save_for_backward(x if h is None else h, weight, rstd)
-        return y if h is None else (y, h)
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dy, dh=None):
-        h, weight, rstd = ctx.saved_tensors
-        need_x, need_w, need_r = ctx.needs_input_grad[:3]
-        dx, dw = dh, None
-        if dy is not None:
-            dx, dw = rms_norm_grad(_as_rows(dy), h, weight, rstd, _as_rows(dh), need_w)
-        return dx if need_x else None, dw, dx if need_r else None, None
-
-
 def rms_norm(x, weight, residual=None, eps=1e-6, stream=None):
     """y[i] = h[i] weight / sqrt(mean(h[i]^2) + eps) with h = x, or, with a
     residual, h = x + residual rounded to their type; returns y, or (y, h).
@@ -152,29 +112,25 @@ def rms_norm(x, weight, residual=None, eps=1e-6, stream=None):
     values of that type or float32.  Sums in float32, y rounded once.
     Differentiable (once).  Asynchronous on `stream` (default: torch's current
     stream)."""
+    eps = float(eps)
+    if stream is None:
+        out = _remembered(NORM, eps, x, weight, residual)
+        if out is not None:
+            return out
     _arguments(x, weight, residual)
-
-    def call():
-        if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or
-                                        (residual is not None and residual.requires_grad)):
-            return _RmsNorm.apply(x, weight, residual, eps)
-        y, h, _ = _forward(x, weight, residual, eps, False)
-        return y if h is None else (y, h)
-    return _on_stream(call, x.device, stream, (x, weight, residual))
+    return _on_stream(lambda: _row_operator("norm", NORM, stream is None, eps, x, weight, residual), x.device, stream,
+                      (x, weight, residual))
 
 
 def rms_norm_i8(x, weight, residual=None, eps=1e-6, stream=None):
     """rms_norm's values in 8 bits: (q, scale), or (q, scale, h) with a residual.
     q: R x K int8, scale: R float32 as i8.i8_quantize makes them, of the values
     before any rounding to 16 bits.  No gradients."""
+    eps = float(eps)
+    if stream is None:
+        out = _remembered(NORM_I8, eps, x, weight, residual)
+        if out is not None:
+            return out
     _arguments(x, weight, residual)
-
-    def call():
-        R, K = x.shape
-        q = torch.empty((R, K), dtype=torch.int8, device=x.device)
-        scale = torch.empty(R, dtype=torch.float32, device=x.device)
-        h = torch.empty((R, K), dtype=x.dtype, device=x.device) if residual is not None else None
-        gemm_rms_norm_i8(_problem(x, weight, residual, eps, q), x.data_ptr(), _address(residual), weight.data_ptr(),
-                         _address(h), q.data_ptr(), scale.data_ptr(), _raw_stream(x.device.index))
-        return (q, scale) if h is None else (q, scale, h)
-    return _on_stream(call, x.device, stream, (x, weight, residual))
+    return _on_stream(lambda: _row_operator("norm_i8", NORM_I8, stream is None, eps, x, weight, residual), x.device, stream,
+                      (x, weight, residual))

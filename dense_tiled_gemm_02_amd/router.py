@@ -12,7 +12,7 @@ import ctypes
 import torch
 
 from . import (GEMM_BF16, GEMM_F16, GEMM_F32, GEMM_SCORE_SIGMOID, GEMM_SCORE_SOFTMAX, _check, gemm_route_problem, lib)
-from .grouped import _need_gpu, _on_stream, _raw_stream
+from .grouped import ROUTE, _need_gpu, _on_stream, _raw_stream, _remembered, _row_operator
 
 _CODES = {torch.float16: GEMM_F16, torch.bfloat16: GEMM_BF16, torch.float32: GEMM_F32}
 SCORES = {"softmax": GEMM_SCORE_SOFTMAX, "sigmoid": GEMM_SCORE_SIGMOID}
@@ -30,16 +30,6 @@ def gemm_route_grad(problem, logits, ids, dweights, dlogits, stream=None):
 
 # ---------------------------------------------------------------- torch convenience
 
-def _problem(logits, top, score, has_bias, groups, top_groups, group_best, renormalize, scale):
-    p = gemm_route_problem()
-    p.R, p.E, p.top = logits.shape[0], logits.shape[1], top
-    p.sl = logits.stride(0)
-    p.groups, p.top_groups, p.group_best = groups, top_groups, group_best
-    p.has_bias, p.renormalize, p.scale = has_bias, 1 if renormalize else 0, scale
-    p.dtype, p.score = _CODES[logits.dtype], SCORES[score]
-    return p
-
-
 def _logits_arg(logits, score):
     if logits.dtype not in _CODES:
         raise TypeError("logits must be float16, bfloat16 or float32, got %s" % logits.dtype)
@@ -47,38 +37,6 @@ def _logits_arg(logits, score):
         raise ValueError("logits must be 2-D with unit stride along the rows, got %s" % (tuple(logits.shape),))
     if score not in SCORES:
         raise ValueError("score must be one of %s, got %r" % (", ".join(SCORES), score))
-
-
-def _choose(p, logits, bias):
-    weights = torch.empty((p.R, p.top), dtype=torch.float32, device=logits.device)
-    ids = torch.empty((p.R, p.top), dtype=torch.int32, device=logits.device)
-    gemm_route(p, logits.data_ptr(), bias.data_ptr() if bias is not None else None, weights.data_ptr(), ids.data_ptr(),
-               _raw_stream(logits.device.index))
-    return weights, ids
-
-
-def _grad(p, dweights, logits, ids):
-    dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    gemm_route_grad(p, logits.data_ptr(), ids.data_ptr(), dweights.data_ptr(), dlogits.data_ptr(),
-                    _raw_stream(logits.device.index))
-    return dlogits
-
-
-class _Route(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, logits, bias, p):
-        weights, ids = _choose(p, logits, bias)
-        ctx.p = p
-        ctx.save_for_backward(logits, ids)
-        ctx.mark_non_differentiable(ids)
-        return weights, ids
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dweights, _):
-        logits, ids = ctx.saved_tensors
-        with torch.cuda.device(logits.device):
-            return _grad(ctx.p, dweights.contiguous(), logits, ids), None, None
 
 
 def route(logits, top, score="softmax", bias=None, groups=1, top_groups=1, group_best=1, renormalize=True, scale=1.0,
@@ -95,18 +53,18 @@ def route(logits, top, score="softmax", bias=None, groups=1, top_groups=1, group
     of -inf or NaN is never chosen; ids that are left over are -1 with weight 0.
     The weights are differentiable (once) for the logits.  Asynchronous on
     `stream` (default: torch's current stream)."""
+    how = (top, SCORES.get(score, -1), groups, top_groups, group_best, 1 if renormalize else 0, float(scale))
+    if stream is None:
+        pair = _remembered(ROUTE, how, logits, bias)
+        if pair is not None:
+            return pair
     _logits_arg(logits, score)
     if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (logits.shape[1],) or
                              (bias.shape[0] > 1 and bias.stride(0) != 1)):
         raise ValueError("bias must be %d contiguous float32 values" % logits.shape[1])
     _need_gpu(logits.device, ("logits", logits), ("bias", bias))
-
-    def call():
-        p = _problem(logits, top, score, 0 if bias is None else 1, groups, top_groups, group_best, renormalize, scale)
-        if logits.requires_grad and torch.is_grad_enabled():
-            return _Route.apply(logits, bias, p)
-        return _choose(p, logits, bias)
-    return _on_stream(call, logits.device, stream, (logits, bias))
+    return _on_stream(lambda: _row_operator("route", ROUTE, stream is None, how, logits, bias), logits.device, stream,
+                      (logits, bias))
 
 
 def route_grad(dweights, logits, ids, score="softmax", renormalize=True, scale=1.0):
@@ -123,5 +81,13 @@ def route_grad(dweights, logits, ids, score="softmax", renormalize=True, scale=1
     _need_gpu(logits.device, ("logits", logits), ("dweights", dweights), ("ids", ids))
 
     def call():
-        return _grad(_problem(logits, ids.shape[1], score, 0, 1, 1, 1, renormalize, scale), dweights, logits, ids)
+        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        p = gemm_route_problem()
+        p.R, p.E, p.top, p.sl = logits.shape[0], logits.shape[1], ids.shape[1], logits.stride(0)
+        p.groups = p.top_groups = p.group_best = 1
+        p.renormalize, p.scale = 1 if renormalize else 0, scale
+        p.dtype, p.score = _CODES[logits.dtype], SCORES[score]
+        gemm_route_grad(p, logits.data_ptr(), ids.data_ptr(), dweights.data_ptr(), dlogits.data_ptr(),
+                        _raw_stream(logits.device.index))
+        return dlogits
     return _on_stream(call, logits.device, None, ())

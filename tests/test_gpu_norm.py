@@ -292,3 +292,31 @@ def test_captured_forward_and_backward():
         got = [t.clone() for t in captured]
         for a, b in zip(got, step()):
             assert torch.equal(a, b)
+
+
+def test_gradients_have_no_gradients():
+    x, w = (rows(3, 64, torch.bfloat16, i).cuda().requires_grad_() for i in (1, 2))
+    dx, = torch.autograd.grad(norm.rms_norm(x, w.detach()[0]).float().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="not differentiable"):
+        dx.float().sum().backward()
+
+
+class Marked(torch.Tensor):
+    """A tensor subclass: the calls that are remembered do not look at it."""
+
+
+def test_other_tensor_types_and_calls_made_twice():
+    x, r, w = rows(5, 200, torch.float16, 1).cuda(), rows(5, 200, torch.float16, 2).cuda(), rows(1, 200, torch.float32, 3)[0].cuda()
+    first = norm.rms_norm(x, w, r), norm.rms_norm_i8(x, w, r), i8.i8_quantize(x)
+    again = norm.rms_norm(x, torch.nn.Parameter(w), r), norm.rms_norm_i8(x, w, r), i8.i8_quantize(x)
+    with torch.no_grad():
+        marked = norm.rms_norm(x.as_subclass(Marked), w, r), norm.rms_norm_i8(x.as_subclass(Marked), w, r), \
+            i8.i8_quantize(x.as_subclass(Marked))
+    for a, b, c in zip(first, again, marked):
+        for s, t, u in zip(a, b, c):
+            assert torch.equal(s.detach(), t.detach()) and torch.equal(s, u.as_subclass(torch.Tensor))
+    # what was not remembered is refused as before
+    with pytest.raises(TypeError):
+        norm.rms_norm(x, w.double(), r)
+    with pytest.raises(Exception, match="eps"):
+        norm.rms_norm(x, w, r, eps=0.0)

@@ -286,3 +286,26 @@ def test_another_stream_and_a_captured_step():
         got = [t.clone() for t in captured]
         for a, b in zip(got, step()):
             assert torch.equal(a, b)
+
+
+def test_gradients_have_no_gradients():
+    l = random_logits(4, 32, "f32", 1).cuda().requires_grad_()
+    dl, = torch.autograd.grad(router.route(l, 3)[0].square().sum(), l, create_graph=True)
+    with pytest.raises(RuntimeError, match="not differentiable"):
+        dl.sum().backward()
+
+
+def test_calls_made_twice():
+    l, bias = random_logits(40, 32, "bf16", 1).cuda(), random_bias(32, 1).cuda()
+    for kw in (dict(), dict(score="sigmoid"), dict(scale=2), dict(renormalize=False), dict(groups=4, top_groups=2, group_best=2)):
+        w, ids = router.route(l, 3, bias=bias, **kw)
+        for _ in range(2):
+            w2, ids2 = router.route(l, 3, bias=bias, **kw)
+            assert torch.equal(w, w2) and torch.equal(ids, ids2)
+    for kw in (dict(score=0), dict(score=1), dict(score=None)):
+        with pytest.raises(ValueError):
+            router.route(l, 3, bias=bias, **kw)
+    for kw in (dict(top=0), dict(top=33), dict(top=1 << 32), dict(groups=5), dict(groups=0), dict(top_groups=2), dict(group_best=3),
+               dict(scale=float("nan")), dict(top=-1)):
+        with pytest.raises(RuntimeError):
+            router.route(l, **{"top": 3, **kw})
