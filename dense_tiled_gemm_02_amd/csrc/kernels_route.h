@@ -19,6 +19,13 @@ struct RouteArgs {
     int32_t sigmoid, renorm;
     float scale;
     uint32_t per_group_inv;   // floor(e per_group_inv / 2^20) = e / (E / groups) for e < E
+    // filled in by launch_route: the launch's first row, doubles of LDS to a row,
+    // and where the groups' lanes lie
+    int64_t first;
+    int32_t spare;
+    int32_t per;              // E / groups
+    int32_t lane_shift;       // a group has 1 << lane_shift lanes
+    int32_t in_lanes;         // 1: whose logits are that group's
 };
 
 struct RouteGradArgs {
@@ -27,6 +34,7 @@ struct RouteGradArgs {
     const float* dw;       // R x top, rows sg elements apart
     void* dl;              // R x E, of the logits' type
     int64_t R, sl, sg, sd;
+    int64_t first;         // the launch's first row (filled in by launch_route_grad)
     int32_t E, top;
     int32_t sigmoid, renorm;
     float scale;

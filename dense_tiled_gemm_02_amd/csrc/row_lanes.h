@@ -1,4 +1,4 @@
-// Reductions over 16 or 64 neighbouring lanes of a wave (gfx950).
+// Reductions over 16, 32 or 64 neighbouring lanes of a wave (gfx950).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -19,15 +19,13 @@ __device__ __forceinline__ uint32_t lane_swap(uint32_t v) {
 // one.  All T lanes must be active; other groups of T need not be.
 template <int T, typename Op>
 __device__ __forceinline__ uint32_t lanes(uint32_t v, Op op) {
-    static_assert(T == 16 || T == 64, "lanes");
+    static_assert(T == 16 || T == 32 || T == 64, "lanes");
     v = op(v, lane_swap<0xB1>(v));
     v = op(v, lane_swap<0x4E>(v));
     v = op(v, lane_swap<0x141>(v));
     v = op(v, lane_swap<0x140>(v));
-    if constexpr (T == 64) {
-        v = op(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), 16)));
-        v = op(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), 32)));
-    }
+    if constexpr (T >= 32) v = op(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), 16)));
+    if constexpr (T == 64) v = op(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), 32)));
     return v;
 }
 

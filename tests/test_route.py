@@ -101,20 +101,22 @@ def oracle(l, top, score="softmax", bias=None, groups=1, top_groups=1, group_bes
     weights, ids = torch.zeros(R, top, dtype=torch.float64), torch.full((R, top), -1, dtype=torch.int32)
     c = p if bias is None else p + bias.double()
     order = l.double() if bias is None else c   # without a bias, scores that 64 bits cannot tell apart go by the logits
+    orders, summands, havings = order.tolist(), c.tolist(), had.tolist()
     for r in range(R):
-        left = [e for e in range(E) if had[r, e]]
+        rank, of_group, having = orders[r], summands[r], havings[r]
+        left = [e for e in range(E) if having[e]]
         if groups > 1:
             per = E // groups
             strength = []
             for k in range(groups):
                 mine = [e for e in left if e // per == k]
-                by = order if group_best == 1 else c
-                best = sorted((by[r, e].item() for e in mine), reverse=True)[:group_best]
+                by = rank if group_best == 1 else of_group
+                best = sorted((by[e] for e in mine), reverse=True)[:group_best]
                 if best:
                     strength.append((-sum(best), k))
             kept = {k for _, k in sorted(strength)[:top_groups]}
             left = [e for e in left if e // per in kept]
-        chosen = sorted(left, key=lambda e: (-order[r, e].item(), e))[:top]
+        chosen = sorted(left, key=lambda e: (-rank[e], e))[:top]
         if not chosen:
             continue
         ids[r, :len(chosen)] = torch.tensor(chosen, dtype=torch.int32)
