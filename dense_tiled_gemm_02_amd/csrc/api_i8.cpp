@@ -17,7 +17,7 @@ struct gemm_i8_plan {
     const dtg::I8TileEntry* tile;     // one of these two, or neither: the kernel for any address
     const dtg::I8FewEntry* few;
     int64_t tiles_m, tiles_n;
-    int group_m, xcds;
+    int group_m, xcds, cus;
 };
 
 namespace {
@@ -76,34 +76,53 @@ bool chunked(const gemm_i8_problem* p) {
 // 32-bit offsets of `rows` rows from a rebased descriptor.
 bool near(int64_t rows, int64_t stride, int64_t K) { return rows * stride + K < (int64_t(1) << 31) - 4096; }
 
+// The smallest tile of at most 64 x 32 whose workgroups the CUs hold at once: K is
+// long beside the tile, and its waves share it out, so that a second round or a
+// larger tile costs more than reading X or W again (us, W from memory):
+//   64 x 1024 x 1024   16 x 16 tiles 3.4, 32 x 32 4.1, 64 x 64 5.3
+//   32 x 4096 x 4096   16 x 32 7.3, 32 x 32 8.0; 16 x 16, two rounds 11
+//   128 x 4096 x 4096  64 x 32 10.2, 32 x 32, two rounds 12.3, 64 x 64 12.1
+//   64 x 14336 x 4096  64 x 64 16.3, 64 x 32, two rounds 20.7
+// Up to 32 rows the widest tile stays on where no tile fits: 32 x 28672 x 8192 42.9
+// us, 64 x 64 46.5.
 const dtg::I8FewEntry* pick_few(const gemm_i8_problem* p, const gemm_device_info* dev) {
-    if (p->M > 64) return nullptr;
-    const int mb = p->M <= 16 ? 1 : p->M <= 32 ? 2 : 4;
-    // two column blocks where one leaves every CU more than a workgroup
-    const int nb = mb > 1 || cdiv(p->N, 16) > dev->cu_count ? 2 : 1;
+    static const struct { int mb, nb, rows; } order[] = {{1, 1, 0}, {1, 2, 0}, {1, 4, 16}, {2, 2, 0}, {2, 4, 32}, {4, 2, 0}};
     int n = 0;
     const dtg::I8FewEntry* t = dtg::i8_few_table(&n);
-    for (int i = 0; i < n; ++i)
-        if (t[i].mb == mb && t[i].nb == nb && t[i].rows >= p->M && near(16 * nb, p->sw, p->K) && near(64, p->sx, p->K))
-            return &t[i];
+    for (const auto& o : order) {
+        // past a tile's rows the next one; tiles of many columns are for few rows
+        if (o.rows ? p->M > o.rows : o.mb > 1 && p->M <= 16 * o.mb / 2) continue;
+        const bool fits = cdiv(p->M, 16 * o.mb) * cdiv(p->N, 16 * o.nb) <= dev->cu_count;
+        if (!fits && !(o.nb == 4 && p->M > 16 * (o.mb - 1))) continue;
+        if (!near(16 * o.nb, p->sw, p->K) || !near(16 * o.mb, p->sx, p->K)) continue;
+        for (int i = 0; i < n; ++i)
+            if (t[i].mb == o.mb && t[i].nb == o.nb) return &t[i];
+    }
     return nullptr;
 }
 
 const dtg::I8TileEntry* pick_tile(const gemm_i8_problem* p, const gemm_device_info* dev, int out) {
-    // rounds of workgroups times a tile's cost relative to 256 x 256, as for the dense tiles
-    static const struct { int bm, bn, stages, per_cu; double cost; } ladder[] = {
-        {256, 256, 2, 1, 1.0}, {256, 128, 3, 1, 0.64}, {128, 256, 3, 1, 0.64},
-        {128, 128, 4, 1, 0.43}, {128, 128, 2, 2, 0.68}, {64, 64, 4, 2, 0.27}};
+    // Rounds of workgroups times a tile's cost relative to 256 x 256, fitted to K =
+    // 4096 (us a round): 256 x 256 53, 256 x 128 29.4, 128 x 256 31, 128 x 128 21.2, 64
+    // x 64 12.7, and 19.4 with two to a CU.  A last round of at most half the CUs goes
+    // in halves (gemm_i8s_mixed_kernel).
+    const int64_t cus = dev->cu_count;
+    auto cost = [&](const dtg::I8TileEntry& e) {
+        const int64_t tiles = cdiv(p->M, e.bm) * cdiv(p->N, e.bn), left = tiles % cus;
+        if (e.mixed) return tiles > cus && left > 0 && 2 * left <= cus ? static_cast<double>(tiles / cus) + 0.56 : 1e18;
+        if (e.bm == 64) {
+            const int64_t two = tiles % (2 * cus);
+            return static_cast<double>(tiles / (2 * cus)) * 0.366 + (two == 0 ? 0.0 : two <= cus ? 0.24 : 0.366);
+        }
+        return static_cast<double>(cdiv(tiles, cus)) * (e.bm + e.bn == 512 ? 1.0 : e.bm == 256 ? 0.56 : e.bn == 256 ? 0.59 : 0.4);
+    };
     int n = 0, best = -1;
     double best_t = 0.0;
     const dtg::I8TileEntry* t = dtg::i8_scaled_table(&n);
     for (int i = 0; i < n; ++i) {
         if (t[i].out != out || !near(t[i].bm, p->sx, p->K) || !near(t[i].bn, p->sw, p->K)) continue;
-        for (const auto& c : ladder) {
-            if (c.bm != t[i].bm || c.bn != t[i].bn || c.stages != t[i].stages) continue;
-            const double cost = static_cast<double>(cdiv(cdiv(p->M, c.bm) * cdiv(p->N, c.bn), int64_t(dev->cu_count) * c.per_cu)) * c.cost;
-            if (best < 0 || cost < best_t) best = i, best_t = cost;
-        }
+        const double c = cost(t[i]);
+        if (best < 0 || c < best_t) best = i, best_t = c;
     }
     return best < 0 ? nullptr : &t[best];
 }
@@ -131,6 +150,7 @@ gemm_status plan_impl(const gemm_i8_problem* given, const gemm_device_info* dev,
         pl->tiles_n = cdiv(p->N, pl->tile->bn);
         pl->group_m = 8;
         pl->xcds = dev->xcd_count > 0 ? dev->xcd_count : 1;
+        pl->cus = dev->cu_count;
     } else {
         pl->tiles_m = cdiv(p->M, pl->few ? 16 * pl->few->mb : 64);
         pl->tiles_n = cdiv(p->N, pl->few ? 16 * pl->few->nb : 64);
@@ -217,6 +237,7 @@ gemm_status gemm_i8_run(const gemm_i8_plan* plan, const int8_t* X, const float* 
         a.sak = a.ldb = 1;
         a.ldd = p.sy;
         a.s = scales;
+        a.cus = plan->cus;
         err = plan->tile->launch(a, plan->tiles_m * plan->tiles_n, on);
     } else {
         dtg::I8RowsArgs a = {};

@@ -19,6 +19,7 @@ struct ScaledI8 {
 // The tile kernels' view: A = X, B = W in pairs of k (see gemm_dma_kernel.h).
 struct ScaledArgs : KArgs {
     ScaledI8 s;
+    int32_t cus;        // of the device: a round of tiles
 };
 
 // The other kernels': strides in bytes (X, W) and elements (Y).
@@ -36,16 +37,17 @@ enum { kOutF16 = 0, kOutBF16 = 1, kOutF32 = 2 };
 typedef hipError_t (*i8_tile_fn)(const ScaledArgs& args, int64_t grid, hipStream_t stream);
 struct I8TileEntry {
     int32_t bm, bn, stages, mfma, waves_m, waves_n, out;
+    int32_t mixed;      // 1: the last, partial round in halves
     i8_tile_fn launch;
     const char* name;
 };
 const I8TileEntry* i8_scaled_table(int* count);
 
-// Few rows: `rows` of X, 16 nb columns to a workgroup.  K and row strides
-// multiples of 16, X and W 16-byte aligned.
+// Tiles of 16 mb rows and 16 nb columns whose waves share out K.  K and row
+// strides multiples of 16, X and W 16-byte aligned.
 typedef hipError_t (*i8_few_fn)(const I8RowsArgs& args, hipStream_t stream);
 struct I8FewEntry {
-    int32_t mb, nb, kb, rows;
+    int32_t mb, nb;
     i8_few_fn launch[3];   // by output type
     const char* name;
 };

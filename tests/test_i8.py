@@ -69,9 +69,12 @@ def test_sizes_at_the_limits_plan():
 
 @pytest.mark.parametrize("kernel, change", [
     ("gemm_i8s_kernel<256,256,64,", dict(M=4096, N=4096, K=4096)),
-    ("i8_few_kernel<1,1,", dict(M=1, N=4096, K=4096)),
-    ("i8_few_kernel<1,2,", dict(M=16, N=8192, K=8192)),
-    ("i8_few_kernel<4,", dict(M=64, N=1024, K=1024)),
+    ("gemm_i8s_mixed_kernel<", dict(M=4096, N=14336, K=4096)), ("gemm_i8s_kernel<64,64,64,", dict(M=256, N=4096, K=4096)),
+    ("gemm_i8s_kernel<128,128,64,", dict(M=2048, N=2048, K=2048)), ("gemm_i8s_kernel<256,128,64,", dict(M=512, N=14336, K=4096)),
+    ("i8_few_kernel<1,1,", dict(M=1, N=4096, K=4096)), ("i8_few_kernel<1,1,", dict(M=64, N=1024, K=1024)),
+    ("i8_few_kernel<1,2,", dict(M=16, N=8192, K=8192)), ("i8_few_kernel<1,4,", dict(M=1, N=28672, K=4096)),
+    ("i8_few_kernel<2,2,", dict(M=32, N=8192, K=8192)), ("i8_few_kernel<2,4,", dict(M=32, N=28672, K=4096)),
+    ("i8_few_kernel<4,2,", dict(M=64, N=8192, K=8192)), ("i8_few_kernel<4,2,", dict(M=128, N=4096, K=4096)),
     ("i8_any_kernel", dict(K=500)), ("i8_any_kernel", dict(sx=520)), ("i8_any_kernel", dict(sw=513)), ("i8_any_kernel", dict(K=0)),
     ("i8_any_kernel", dict(M=1, N=64, K=17)),
     # rows so far apart that 32-bit offsets of a tile would not reach them
