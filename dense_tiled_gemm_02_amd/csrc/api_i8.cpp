@@ -141,6 +141,7 @@ gemm_status plan_impl(const gemm_i8_problem* given, const gemm_device_info* dev,
     if (!pl) return fail(GEMM_ERR_INVALID_ARG, "out of host memory");
     pl->prob = *p;
     pl->out = p->out == GEMM_F32 ? dtg::kOutF32 : p->out == GEMM_BF16 ? dtg::kOutBF16 : dtg::kOutF16;
+    pl->cus = dev->cu_count;
     if (chunked(p)) {
         pl->few = pick_few(p, dev);
         if (!pl->few) pl->tile = pick_tile(p, dev, pl->out);
@@ -150,7 +151,6 @@ gemm_status plan_impl(const gemm_i8_problem* given, const gemm_device_info* dev,
         pl->tiles_n = cdiv(p->N, pl->tile->bn);
         pl->group_m = 8;
         pl->xcds = dev->xcd_count > 0 ? dev->xcd_count : 1;
-        pl->cus = dev->cu_count;
     } else {
         pl->tiles_m = cdiv(p->M, pl->few ? 16 * pl->few->mb : 64);
         pl->tiles_n = cdiv(p->N, pl->few ? 16 * pl->few->nb : 64);
@@ -251,7 +251,7 @@ gemm_status gemm_i8_run(const gemm_i8_plan* plan, const int8_t* X, const float* 
         a.lx = p.sx;
         a.lw = p.sw;
         a.ly = p.sy;
-        err = plan->few && aligned ? plan->few->launch[plan->out](a, on) : dtg::launch_i8_any(a, plan->out, on);
+        err = plan->few && aligned ? plan->few->launch[plan->out](a, on) : dtg::launch_i8_any(a, plan->out, plan->cus, on);
     }
     return err == hipSuccess ? GEMM_OK : fail(GEMM_ERR_HIP, "launch of the int8 product: %s", hipGetErrorString(err));
 }

@@ -2,11 +2,17 @@
 // direct-to-LDS kernels do not take: K, row strides or bases that are no
 // multiples of 16 bytes.
 //
-// 64 x 64 outputs to a workgroup of four waves, 128 k a step.  Every chunk of
-// 16 k is one load at its own address, whatever that is, through registers one
-// step ahead into one of two LDS stages; the chunk that K cuts is loaded byte by
-// byte.  Rows past the operands read the last row, and what they make is not
-// stored.  The sums are exact (int32), so nothing depends on their order.
+// 64 x 64 outputs to a workgroup, 128 k a step.  Every chunk of 16 k is one load
+// at its own address, whatever that is, through registers one step ahead into one
+// of two LDS stages.  Rows past the operands read the last row, and what they make is not stored.  Bound by the
+// latency of a step, not by bytes, so where the tiles are at most one to a CU KG
+// groups of four waves take the steps in turn, each with its own stages, and
+// their sums meet in LDS.  The sums are exact (int32), so nothing depends on
+// their order.
+//
+// 777 x 1003 x 2005, rows at any byte, 13.1 us; rows of whole words 9.7 us (loads at
+// other addresses take longer; whole words around them, shifted, 12.2 and 12.3).
+// Two or three steps ahead: 13.5 and 14.8 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -28,10 +34,12 @@ constexpr int kChunks = kStep / 16;                                // to a row
 constexpr int kLoads = kTile * kChunks / kThreads;                 // of an operand, to a thread
 constexpr int kStage = kTile * kStep;                              // bytes of an operand
 
-template <int OUT>
-__global__ __launch_bounds__(kThreads) void i8_any_kernel(I8RowsArgs a, int tiles_n) {
-    __shared__ __attribute__((aligned(16))) uint8_t smem[2 * 2 * kStage];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+template <int KG, int OUT>
+__global__ __launch_bounds__(KG * kThreads) void i8_any_kernel(I8RowsArgs a, int tiles_n) {
+    __shared__ __attribute__((aligned(16))) uint8_t all[KG * 2 * 2 * kStage];
+    const int group = threadIdx.x / kThreads;   // whole waves
+    const int tid = threadIdx.x % kThreads, lane = tid & 63, wave = tid >> 6;
+    uint8_t* const smem = all + group * 2 * 2 * kStage;
     const int wm = wave >> 1, wn = wave & 1;
     const int64_t tile = blockIdx.x;
     const int m0 = static_cast<int>(tile / tiles_n) * kTile, n0 = static_cast<int>(tile % tiles_n) * kTile;
@@ -48,29 +56,53 @@ __global__ __launch_bounds__(kThreads) void i8_any_kernel(I8RowsArgs a, int tile
         at[i] = 16 * c;
         lds[i] = row * kStep + 16 * (c ^ swz<kChunks>(row));
     }
+    // A chunk that K cuts is the row's last 16 bytes, moved down when it is staged;
+    // one past K is those, moved out.  (Loads under a condition would wait for one
+    // another: 16.6 us in place of 13.7 at 777 x 1003 x 2005.)
     u32x4 reg[2][kLoads];
     auto load = [&](int k0) {
+        if (K >= 16) {
+#pragma unroll
+            for (int o = 0; o < 2; ++o)
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) {
+                    const int k = k0 + at[i];
+                    reg[o][i] = reinterpret_cast<const Loose16*>(src[o][i] + (k + 16 <= K ? k : K - 16))->v;
+                }
+        } else {   // one step of one chunk
+#pragma unroll
+            for (int o = 0; o < 2; ++o)
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) {
+                    uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+                    for (int e = 0; e < K; ++e) {
+                        const uint64_t c = k0 + at[i] == 0 ? static_cast<uint8_t>(src[o][i][e]) : 0;
+                        (e < 8 ? lo : hi) |= c << (8 * (e & 7));
+                    }
+                    const u32x4 v = {static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
+                                     static_cast<uint32_t>(hi >> 32)};
+                    reg[o][i] = v;
+                }
+        }
+    };
+    auto store = [&](int s, int k0) {
 #pragma unroll
         for (int o = 0; o < 2; ++o)
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                const int k = k0 + at[i];
-                u32x4 v = {0u, 0u, 0u, 0u};
-                if (k + 16 <= K) {
-                    v = reinterpret_cast<const Loose16*>(src[o][i] + k)->v;
-                } else if (k < K) {
-#pragma unroll
-                    for (int e = 0; e < 15; ++e)
-                        if (k + e < K) v[e / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(src[o][i][k + e])) << (8 * (e % 4));
+                u32x4 v = reg[o][i];
+                if (k0 + kStep > K && K >= 16) {
+                    const int over = k0 + at[i] + 16 - K, sh = 8 * over;   // bits to move down
+                    const uint64_t lo = v[0] | static_cast<uint64_t>(v[1]) << 32, hi = v[2] | static_cast<uint64_t>(v[3]) << 32;
+                    const uint64_t up = over >= 16 ? 0 : hi >> (sh & 63);
+                    const uint64_t down = over >= 8 ? up : (lo >> (sh & 63)) | (hi << 1 << (63 - (sh & 63)));
+                    const uint64_t l = over <= 0 ? lo : down, h = over <= 0 ? hi : over >= 8 ? 0 : up;
+                    v = u32x4{static_cast<uint32_t>(l), static_cast<uint32_t>(l >> 32), static_cast<uint32_t>(h),
+                              static_cast<uint32_t>(h >> 32)};
                 }
-                reg[o][i] = v;
+                *reinterpret_cast<u32x4*>(smem + (2 * s + o) * kStage + lds[i]) = v;
             }
-    };
-    auto store = [&](int s) {
-#pragma unroll
-        for (int o = 0; o < 2; ++o)
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) *reinterpret_cast<u32x4*>(smem + (2 * s + o) * kStage + lds[i]) = reg[o][i];
     };
 
     f32x4 acc[2][2];   // int32 bits; [m block][n block], a lane: one m, four n
@@ -79,11 +111,12 @@ __global__ __launch_bounds__(kThreads) void i8_any_kernel(I8RowsArgs a, int tile
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    const int steps = (K + kStep - 1) / kStep;
-    if (steps > 0) load(0);
+    // of every group as many: steps past K are zeros
+    const int steps = ((K + kStep - 1) / kStep + KG - 1) / KG;
+    if (steps > 0) load(group * kStep);
     for (int s = 0; s < steps; ++s) {
-        store(s & 1);
-        if (s + 1 < steps) load((s + 1) * kStep);
+        store(s & 1, (s * KG + group) * kStep);
+        if (s + 1 < steps) load(((s + 1) * KG + group) * kStep);
         __syncthreads();   // the readers of this stage two steps ago passed the previous barrier
         const uint8_t *x = smem + 2 * (s & 1) * kStage, *w = x + kStage;
 #pragma unroll
@@ -101,6 +134,24 @@ __global__ __launch_bounds__(kThreads) void i8_any_kernel(I8RowsArgs a, int tile
                 for (int j = 0; j < 2; ++j) acc[i][j] = mfma_i8<16>(fw[j], fx[i], acc[i][j]);
         }
     }
+    if constexpr (KG > 1) {
+        typedef int i32x4 __attribute__((ext_vector_type(4)));
+        i32x4* const sums = reinterpret_cast<i32x4*>(all);
+        __syncthreads();   // every group is past its last operand reads
+        if (group > 0) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) sums[((group - 1) * 4 + b) * kThreads + tid] = __builtin_bit_cast(i32x4, acc[b / 2][b % 2]);
+        }
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            i32x4 v = __builtin_bit_cast(i32x4, acc[b / 2][b % 2]);
+#pragma unroll
+            for (int g = 0; g < KG - 1; ++g) v += sums[(g * 4 + b) * kThreads + tid];
+            acc[b / 2][b % 2] = __builtin_bit_cast(f32x4, v);
+        }
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int m = m0 + wm * 32 + i * 16 + (lane & 15);
@@ -111,16 +162,21 @@ __global__ __launch_bounds__(kThreads) void i8_any_kernel(I8RowsArgs a, int tile
     }
 }
 
+template <int KG>
+hipError_t launch(const I8RowsArgs& a, int out, int tiles, int tiles_n, hipStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(tiles)), block(KG * kThreads);
+    if (out == kOutF32) hipLaunchKernelGGL((i8_any_kernel<KG, kOutF32>), grid, block, 0, stream, a, tiles_n);
+    else if (out == kOutBF16) hipLaunchKernelGGL((i8_any_kernel<KG, kOutBF16>), grid, block, 0, stream, a, tiles_n);
+    else hipLaunchKernelGGL((i8_any_kernel<KG, kOutF16>), grid, block, 0, stream, a, tiles_n);
+    return hipGetLastError();
+}
+
 }  // namespace
 
-hipError_t launch_i8_any(const I8RowsArgs& a, int out, hipStream_t stream) {
+hipError_t launch_i8_any(const I8RowsArgs& a, int out, int cus, hipStream_t stream) {
     const int64_t tm = (static_cast<int64_t>(a.M) + kTile - 1) / kTile, tn = (static_cast<int64_t>(a.N) + kTile - 1) / kTile;
-    const dim3 grid(static_cast<unsigned>(tm * tn)), block(kThreads);
-    const int n = static_cast<int>(tn);
-    if (out == kOutF32) hipLaunchKernelGGL((i8_any_kernel<kOutF32>), grid, block, 0, stream, a, n);
-    else if (out == kOutBF16) hipLaunchKernelGGL((i8_any_kernel<kOutBF16>), grid, block, 0, stream, a, n);
-    else hipLaunchKernelGGL((i8_any_kernel<kOutF16>), grid, block, 0, stream, a, n);
-    return hipGetLastError();
+    if (tm * tn <= cus) return launch<4>(a, out, static_cast<int>(tm * tn), static_cast<int>(tn), stream);
+    return launch<1>(a, out, static_cast<int>(tm * tn), static_cast<int>(tn), stream);
 }
 
 }  // namespace dtg

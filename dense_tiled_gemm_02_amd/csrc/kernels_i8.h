@@ -54,6 +54,6 @@ struct I8FewEntry {
 const I8FewEntry* i8_few_table(int* count);
 
 // Sizes, strides and addresses of any kind.
-hipError_t launch_i8_any(const I8RowsArgs& a, int out, hipStream_t stream);
+hipError_t launch_i8_any(const I8RowsArgs& a, int out, int cus, hipStream_t stream);
 
 }  // namespace dtg
