@@ -6,13 +6,14 @@
 //     s = max |y| / 127,  q = y / s to the nearest     (int8 output)
 //
 // All of it from one read: T threads hold the row in registers, C chunks of 8
-// values each, with the sums across them through the wave's lanes and, where a
-// row takes more than a wave, one LDS word per wave and one barrier.  Bound by
-// memory: x, r are read and y or q (and h) are written once.  Rows longer than
-// the registers hold are read again for each pass (C = 0).
+// values each, packed as they are stored (what is summed has been rounded to 16
+// bits), with the sums across them through the wave's lanes and, where a row
+// takes more than a wave, one LDS word per wave and one barrier.  Bound by memory:
+// x, r are read and y or q (and h) are written once.  Rows longer than the
+// registers hold are read again for each pass (C = 0).
 //
-// The quotient y / s is an IEEE division and the scale that it is divided by is
-// the stored one, so q is the nearest step of the scale that a product uses.
+// The quotient y / s is defined as an IEEE division by the stored scale, rounded
+// to the nearest integer; see steps_of for how most of it is done without one.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -114,7 +115,20 @@ __device__ __forceinline__ u32x4 narrow8(const float (&v)[8]) {
     return u;
 }
 
-// Elements k .. k + 7 of the weights.
+// Elements k .. k + 7 of the weights, all of them there.
+template <bool BF16>
+__device__ __forceinline__ void whole_weights8(const void* w, int w32, int k, float (&v)[8]) {
+    if (w32) {
+        const float* p = static_cast<const float*>(w) + k;
+        const f32x4 lo = reinterpret_cast<const LooseF4*>(p)->v, hi = reinterpret_cast<const LooseF4*>(p + 4)->v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = lo[e], v[4 + e] = hi[e];
+    } else {
+        widen8<BF16>(reinterpret_cast<const Loose16*>(static_cast<const uint16_t*>(w) + k)->v, v);
+    }
+}
+
+// Elements k .. k + 7 of the weights (zeros past the end).
 template <bool BF16>
 __device__ __forceinline__ void weights8(const void* w, int w32, int k, int K, float (&v)[8]) {
     if (w32) {
@@ -136,121 +150,170 @@ __device__ __forceinline__ void weights8(const void* w, int w32, int k, int K, f
 // 1e19) is taken again, scaled by 2^-200.
 constexpr float kSmaller = 0x1p-100f;
 
+// Eight quotients v / s as bytes.  v times the reciprocal of s, added to 1.5 x 2^23,
+// leaves the nearest integer in the sum's low bits; it is the division's wherever
+// the product is further than 2^-15 from halfway between two integers (both are
+// within 2^-23 of the quotient, relative, and that is at most 127 and a bit).
+// Chunks that hold a closer one, one in several hundred, are divided.  Scales so
+// small that the reciprocal overflows or the quotients pass 127 are, too.
+__device__ __forceinline__ u32x2 steps_of(const float (&v)[8], float s, float inv) {
+    constexpr float magic = 12582912.0f;
+    uint32_t b[8];
+    float worst = s < 0x1p-100f ? 1.0f : 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float t = fmaf(v[e], inv, magic);
+        worst = fmaxf(worst, fabsf(fmaf(v[e], inv, magic - t)));
+        b[e] = __float_as_uint(t);
+    }
+    if (__builtin_expect(!(worst < 0.5f - 0x1p-15f), 0)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float n = s > 0.0f ? fminf(fmaxf(rintf(v[e] / s), -127.0f), 127.0f) : 0.0f;
+            b[e] = static_cast<uint32_t>(static_cast<int>(n));
+        }
+    }
+    u32x2 u;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const uint32_t lo = __builtin_amdgcn_perm(b[4 * e + 1], b[4 * e], 0x0c0c0400), hi = __builtin_amdgcn_perm(b[4 * e + 3], b[4 * e + 2], 0x0c0c0400);
+        u[e] = lo | hi << 16;
+    }
+    return u;
+}
+
 template <bool BF16, int T, int C, bool NORM, bool QUANT>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void rows_kernel(RowsArgs a) {
     constexpr int THREADS = T < 256 ? 256 : T, ROWS = THREADS / T;
     __shared__ uint32_t meet_words[T > 64 ? 2 * (T / 64) : 1];
     Meet<T> meet{meet_words};
     const int t = threadIdx.x % T, K = a.K;
+    const bool odd = K % 8 != 0;
 
     for (int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS; first < a.R; first += static_cast<int64_t>(gridDim.x) * ROWS) {
         const int64_t row = first + threadIdx.x / T;
         const bool live = row < a.R;
         const int Kr = live ? K : 0;   // lanes past the last row touch nothing
-        const uint16_t* x = a.x + (live ? row : 0) * a.sx;
-        const uint16_t* r = a.r ? a.r + (live ? row : 0) * a.sr : nullptr;
-        uint16_t* h = a.r ? a.h + (live ? row : 0) * a.sh : nullptr;
+        const int64_t at = live ? row : 0;
+        const uint16_t* x = a.x + at * a.sx;
+        const uint16_t* r = a.r ? a.r + at * a.sr : nullptr;
+        uint16_t* h = a.r ? a.h + at * a.sh : nullptr;
 
-        // the row's values at k .. k + 7, summed and rounded to the stream's type
-        auto fetch = [&](int k, float (&v)[8]) {
-            const u32x4 ux = load8(x, k, Kr);
-            widen8<BF16>(ux, v);
-            if (r) {
-                float v2[8];
-                widen8<BF16>(load8(r, k, Kr), v2);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] += v2[e];
-                const u32x4 u = narrow8<BF16>(v);
-                store8(h, k, Kr, u);
-                widen8<BF16>(u, v);
+        // Chunk k .. k + 7 of a row held in registers starts at `from`: the last one
+        // moves back to end with the row (whole loads and stores only), and its
+        // first k - from values are the chunk's before it, not to be summed again.
+        auto from = [&](int k) { return k + 8 <= K ? k : K - 8; };
+        auto load = [&](const uint16_t* p, int k) {
+            if constexpr (C > 0) return k < Kr ? reinterpret_cast<const Loose16*>(p + from(k))->v : u32x4{0u, 0u, 0u, 0u};
+            else return load8(p, k, Kr);
+        };
+        auto store = [&](uint16_t* p, int k, u32x4 u) {
+            if constexpr (C > 0) {
+                if (k < Kr) reinterpret_cast<Loose16*>(p + from(k))->v = u;
+            } else {
+                store8(p, k, Kr, u);
             }
         };
-        float keep[C > 0 ? C : 1][8];
-        // fn(k, values) over this thread's chunks; `again`: the row has been summed
+        // the row's values at a chunk, summed and rounded to the stream's type
+        auto fetch = [&](int k) {
+            u32x4 u = load(x, k);
+            if (r) {
+                float v[8], v2[8];
+                widen8<BF16>(u, v);
+                widen8<BF16>(load(r, k), v2);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] += v2[e];
+                u = narrow8<BF16>(v);
+                store(h, k, u);
+            }
+            return u;
+        };
+        u32x4 keep[C > 0 ? C : 1];
+        // fn(k, chunk) over this thread's chunks; `again`: the row has been summed
         auto chunks = [&](bool again, auto&& fn) {
             if constexpr (C > 0) {
 #pragma unroll
                 for (int c = 0; c < C; ++c) fn(8 * (t + c * T), keep[c]);
             } else {
-                for (int k = 8 * t; k < Kr; k += 8 * T) {
-                    float v[8];
-                    if (!again) fetch(k, v);
-                    else widen8<BF16>(load8(r ? h : x, k, Kr), v);
-                    fn(k, v);
-                }
+                for (int k = 8 * t; k < Kr; k += 8 * T) fn(k, again ? load(r ? h : x, k) : fetch(k));
             }
         };
         if constexpr (C > 0) {
 #pragma unroll
-            for (int c = 0; c < C; ++c) fetch(8 * (t + c * T), keep[c]);
+            for (int c = 0; c < C; ++c) keep[c] = fetch(8 * (t + c * T));
         }
 
         float rstd = 1.0f;
         if constexpr (NORM) {
-            float ss = 0.0f;
-            chunks(false, [&](int, float (&v)[8]) {
+            auto squares = [&](bool again, float by) {
+                float ss = 0.0f;
+                chunks(again, [&](int k, u32x4 u) {
+                    float v[8];
+                    widen8<BF16>(u, v);
+                    const int skip = C > 0 && odd ? k - from(k) : 0;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-            });
-            ss = meet.sum(ss);
-            if (__builtin_expect(ss == kInf && BF16, 0)) {
-                float small = 0.0f;
-                chunks(true, [&](int, float (&v)[8]) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) small = fmaf(v[e] * kSmaller, v[e] * kSmaller, small);
+                    for (int e = 0; e < 8; ++e) {
+                        const float w = (C > 0 && odd && e < skip ? 0.0f : v[e]) * by;
+                        ss = fmaf(w, w, ss);
+                    }
                 });
-                // rows of one wave meet by lanes alone; of several, every thread of the workgroup is here
-                rstd = kSmaller / sqrtf(meet.sum(small) / static_cast<float>(K));
-            } else {
-                rstd = 1.0f / sqrtf(ss / static_cast<float>(K) + a.eps);
-            }
+                return meet.sum(ss);
+            };
+            const float ss = squares(false, 1.0f);
+            // rows of one wave meet by lanes alone; of several, every thread of the workgroup is here
+            if (BF16 && __builtin_expect(ss == kInf, 0)) rstd = kSmaller / sqrtf(squares(true, kSmaller) / static_cast<float>(K));
+            else rstd = 1.0f / sqrtf(ss / static_cast<float>(K) + a.eps);
             if (a.rstd && live && t == 0) a.rstd[row] = rstd;
         }
-        auto normed = [&](int k, float (&v)[8]) {
+        auto values = [&](int k, u32x4 u, float (&v)[8]) {
+            widen8<BF16>(u, v);
             if constexpr (NORM) {
                 float w[8];
-                weights8<BF16>(a.w, a.w32, k, Kr, w);
+                if constexpr (C > 0) whole_weights8<BF16>(a.w, a.w32, k < Kr ? from(k) : 0, w);
+                else weights8<BF16>(a.w, a.w32, k, Kr, w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = v[e] * rstd * w[e];
             }
         };
         if constexpr (!QUANT) {
-            uint16_t* y = a.y + (live ? row : 0) * a.sy;
-            chunks(true, [&](int k, float (&v)[8]) {
-                normed(k, v);
-                store8(y, k, Kr, narrow8<BF16>(v));
+            uint16_t* y = a.y + at * a.sy;
+            chunks(true, [&](int k, u32x4 u) {
+                float v[8];
+                values(k, u, v);
+                store(y, k, narrow8<BF16>(v));
             });
         } else {
-            float most = 0.0f;
-            chunks(NORM, [&](int k, float (&v)[8]) {
-                normed(k, v);
+            uint32_t most = 0;   // as bits: see Max
+            if constexpr (NORM) {
+                chunks(true, [&](int k, u32x4 u) {
+                    float v[8];
+                    values(k, u, v);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    most = __uint_as_float(Max()(__float_as_uint(most), __float_as_uint(fabsf(v[e]))));
-            });
-            most = meet.most(most);
+                    for (int e = 0; e < 8; ++e) most = Max()(most, __float_as_uint(fabsf(v[e])));
+                });
+            } else {   // 16-bit magnitudes, two to a word
+                typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+                u16x2 two = {0, 0};
+                chunks(false, [&](int, u32x4 u) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) two = __builtin_elementwise_max(two, __builtin_bit_cast(u16x2, u[e] & 0x7fff7fffu));
+                });
+                most = __float_as_uint(widen<BF16>(two[0] > two[1] ? two[0] : two[1]));
+            }
+            const float largest = __uint_as_float(meet.all(most, Max()));
             // a row with an infinity or a NaN has no steps: its scale says so
-            const bool fine = __float_as_uint(most) < __float_as_uint(kInf);
-            const float s = fine ? most / 127.0f : __builtin_nanf("");
-            const bool steps = s > 0.0f;
+            const bool fine = __float_as_uint(largest) < __float_as_uint(kInf);
+            const float s = fine ? largest / 127.0f : __builtin_nanf("");
+            const float by = fine ? s : 0.0f, inv = 1.0f / by;
             if (live && t == 0) a.scale[row] = s;
-            int8_t* q = a.q + (live ? row : 0) * a.sy;
-            chunks(true, [&](int k, float (&v)[8]) {
-                if constexpr (C == 0) normed(k, v);
-                int i[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float n = rintf(v[e] / s);   // in the smallest scales past 127
-                    i[e] = steps ? static_cast<int>(fminf(fmaxf(n, -127.0f), 127.0f)) : 0;
-                }
-                u32x2 u;
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    u[e] = (i[4 * e] & 255) | (i[4 * e + 1] & 255) << 8 | (i[4 * e + 2] & 255) << 16 |
-                           static_cast<uint32_t>(i[4 * e + 3]) << 24;
-                if (k + 8 <= Kr) {
-                    reinterpret_cast<Loose8*>(q + k)->v = u;
-                } else if (k < Kr) {
+            int8_t* q = a.q + at * a.sy;
+            chunks(true, [&](int k, u32x4 chunk) {
+                float v[8];
+                values(k, chunk, v);
+                const u32x2 u = steps_of(v, by, inv);
+                if (C > 0 ? k < Kr : k + 8 <= Kr) {
+                    reinterpret_cast<Loose8*>(q + (C > 0 ? from(k) : k))->v = u;
+                } else if (C == 0 && k < Kr) {
 #pragma unroll
                     for (int e = 0; e < 7; ++e)
                         if (k + e < Kr) q[k + e] = static_cast<int8_t>(u[e / 4] >> (8 * (e % 4)));
@@ -407,11 +470,34 @@ __global__ __launch_bounds__(64 * kSumWaves) void norm_weight_grad_kernel(const 
     else static_cast<uint16_t*>(dw)[k] = narrow<KIND == 1>(v);
 }
 
-// Threads and chunks of 8 to a row of K.
+// Threads and chunks of 8 to a row of K, by measurement (us of quantization, norm
+// with residual, the same into int8; a CU holds 2048 threads, and wants several
+// rows, of which one waits for memory while another is worked on):
+//   8192 x 4096    256 x 2  18, 45, 45    512 x 1  21, 45, 46    256 x 4   18, 50, 67
+//   4096 x 8192    512 x 2  18, 46, 46    256 x 4  17, 48, 52    1024 x 1  25, 50, 49
+//   4096 x 14336   512 x 4  29, 91, 93    256 x 8  30, 100, 125  1024 x 2  32, 93, 100
+//   16384 x 2048   256 x 1  20, 46, 45    64 x 4   17, 48, 50    512 x 1   31, 54, 66
+// (a copy's rate: 20, 54, 48 us for the first two and the last, 36, 95, 83 for the
+// third).  Few rows want more threads to each:
+//   1 x 4096       512 x 1  2.6, 2.8, 3.5   256 x 2  2.6, 3.3, 4.0
+//   16 x 14336     1024 x 2  3.4, 4.4, 5.5  512 x 4  3.1, 5.4, 6.5
 struct Shape {
     int t, c;
 };
-Shape shape_of(int64_t K) {
+Shape shape_of(int64_t R, int64_t K) {
+    if (K < 8) return {16, 0};
+    if (K <= 128) return {16, 1};
+    if (K <= 512) return {64, 1};
+    if (K <= 1024) return {64, 2};
+    if (K <= 2048) return {256, 1};
+    if (K <= 4096) return R <= 512 ? Shape{512, 1} : Shape{256, 2};
+    if (K <= 8192) return {512, 2};
+    if (K <= 16384) return R <= 256 ? Shape{1024, 2} : Shape{512, 4};
+    if (K <= 32768) return {1024, 4};
+    return {1024, 0};
+}
+// Of the gradient, whose sums for dw take registers, too.
+Shape grad_shape_of(int64_t K) {
     if (K <= 128) return {16, 1};
     if (K <= 512) return {64, 1};
     if (K <= 1024) return {64, 2};
@@ -422,11 +508,26 @@ Shape shape_of(int64_t K) {
     return {1024, 0};
 }
 
-template <typename Fn>
-hipError_t with_shape(int64_t K, Fn&& fn) {
-    const Shape s = shape_of(K);
 #define DTG_SHAPE(T, C) \
     if (s.t == T && s.c == C) return fn(std::integral_constant<int, T>{}, std::integral_constant<int, C>{});
+template <typename Fn>
+hipError_t with_shape(Shape s, Fn&& fn) {
+    DTG_SHAPE(16, 0)
+    DTG_SHAPE(16, 1)
+    DTG_SHAPE(64, 1)
+    DTG_SHAPE(64, 2)
+    DTG_SHAPE(256, 1)
+    DTG_SHAPE(256, 2)
+    DTG_SHAPE(512, 1)
+    DTG_SHAPE(512, 2)
+    DTG_SHAPE(512, 4)
+    DTG_SHAPE(1024, 2)
+    DTG_SHAPE(1024, 4)
+    DTG_SHAPE(1024, 0)
+    return hipErrorInvalidValue;
+}
+template <typename Fn>
+hipError_t with_grad_shape(Shape s, Fn&& fn) {
     DTG_SHAPE(16, 1)
     DTG_SHAPE(64, 1)
     DTG_SHAPE(64, 2)
@@ -435,15 +536,15 @@ hipError_t with_shape(int64_t K, Fn&& fn) {
     DTG_SHAPE(1024, 1)
     DTG_SHAPE(1024, 2)
     DTG_SHAPE(1024, 0)
-#undef DTG_SHAPE
     return hipErrorInvalidValue;
 }
+#undef DTG_SHAPE
 
 constexpr int64_t kMostGroups = int64_t(1) << 20;   // workgroups of a launch; each then takes several rows
 
 template <bool BF16, bool NORM, bool QUANT>
 hipError_t launch_rows_as(const RowsArgs& a, hipStream_t stream) {
-    return with_shape(a.K, [&](auto t_tag, auto c_tag) {
+    return with_shape(shape_of(a.R, a.K), [&](auto t_tag, auto c_tag) {
         constexpr int T = decltype(t_tag)::value, C = decltype(c_tag)::value;
         constexpr int THREADS = T < 256 ? 256 : T, ROWS = THREADS / T;
         const int64_t need = (a.R + ROWS - 1) / ROWS;
@@ -462,14 +563,14 @@ hipError_t launch_rows(const RowsArgs& a, int bf16, hipStream_t stream) {
 }
 
 int64_t norm_grad_parts(int64_t R, int64_t K) {
-    const Shape s = shape_of(K);
+    const Shape s = grad_shape_of(K);
     const int64_t rows = s.t < 256 ? 256 / s.t : 1, need = (R + rows - 1) / rows;
     const int64_t most = s.t > 256 ? 256 : 1024;   // a CU's worth of threads each
     return need < most ? need : most;
 }
 
 hipError_t launch_norm_grad(const NormGradArgs& a, int bf16, hipStream_t stream) {
-    return with_shape(a.K, [&](auto t_tag, auto c_tag) {
+    return with_grad_shape(grad_shape_of(a.K), [&](auto t_tag, auto c_tag) {
         constexpr int T = decltype(t_tag)::value, C = decltype(c_tag)::value;
         const dim3 grid(static_cast<unsigned>(norm_grad_parts(a.R, a.K))), block(T < 256 ? 256 : T);
         if (bf16) hipLaunchKernelGGL((norm_grad_kernel<true, T, C>), grid, block, 0, stream, a);

@@ -2,9 +2,8 @@
 
 Tolerances.  u is half a step of the output's type relative to the value, the
 one rounding of an output.  In fp32 (steps of 2^-24): a sum of K squares goes
-through at most 40 additions in a row for the sizes here (up to 20 chunks of
-8 a thread, in chains of fused additions of 8 x 5 at the longest, then 10 across
-threads), its square root halves that, and a division and two products follow:
+through at most 50 additions in a row for the sizes here (up to 5 chunks of 8 a
+thread, then 10 across threads), its square root halves that, and a division and two products follow:
 64 x 2^-24 = 2^-18 covers all of them."""
 import pytest
 import torch
@@ -17,8 +16,8 @@ pytestmark = pytest.mark.gpu
 TYPES = {"f16": torch.float16, "bf16": torch.bfloat16}
 FP32 = 2.0 ** -18
 # every number of threads and chunks to a row, one value more and less, and rows read again
-WIDTHS = [1, 2, 7, 8, 127, 128, 129, 500, 512, 513, 1000, 1024, 1025, 2048, 2049, 4095, 4096, 4097, 8192, 8200, 16384,
-          16385, 20001]
+WIDTHS = [1, 2, 7, 8, 9, 15, 127, 128, 129, 500, 512, 513, 1000, 1024, 1025, 2048, 2049, 4095, 4096, 4097, 8192, 8200, 16384,
+          16385, 20001, 32768, 33001]
 EPS = 1e-5
 
 
@@ -320,3 +319,47 @@ def test_other_tensor_types_and_calls_made_twice():
         norm.rms_norm(x, w.double(), r)
     with pytest.raises(Exception, match="eps"):
         norm.rms_norm(x, w, r, eps=0.0)
+
+
+def test_many_rows_of_every_kind_of_row():
+    """The shapes for more rows than a round, against the ones for few, bit by bit, and by value."""
+    for K in (3000, 4096, 12001, 16384):
+        print("many rows", K, flush=True)
+        x, r = rows(700, K, torch.bfloat16, K).cuda(), rows(700, K, torch.bfloat16, K + 1).cuda()
+        w = rows(1, K, torch.float32, 6)[0].cuda()
+        q, scale = i8.i8_quantize(x)
+        some = i8.i8_quantize(x[300:400])
+        assert torch.equal(q[300:400], some[0]) and torch.equal(scale[300:400], some[1])
+        y, h = norm.rms_norm(x, w, r, eps=EPS)
+        check_y(y[-5:].cpu(), h[-5:].cpu(), w.cpu())
+        assert torch.equal(h, (x.float() + r.float()).bfloat16())
+        q, scale, h2 = norm.rms_norm_i8(x, w, r, eps=EPS)
+        h64 = h[-5:].cpu().double()
+        check_rows(q[-5:], scale[-5:], h64 * w.cpu().double() / torch.sqrt(h64.square().mean(1, keepdim=True) + EPS), FP32)
+        assert torch.equal(h, h2)
+
+
+def test_quotients_halfway_between_two_steps():
+    """Values whose quotient is halfway, or next to it: rounded as an IEEE division's."""
+    for dt in TYPES.values():
+        x = torch.arange(-127, 128).to(dt).repeat(40, 1)
+        x[:, 3] = 127
+        for i in range(1, 40):
+            x[i] = (x[0].float() * (0.5 + i / 64)).to(dt)
+            x[i, 3] = 127
+        x[10] = (x[0].float() - 0.5).to(dt)
+        x[10, 3] = 127
+        x[11] = x[10] * 2.0 ** -8
+        q, scale = i8.i8_quantize(x.cuda())
+        s = x.float().abs().amax(1) / 127
+        assert torch.equal(scale.cpu(), s)
+        assert torch.equal(q.cpu().float(), (x.float() / s[:, None]).round().clamp(-127, 127))
+    # the smallest scales: their reciprocal is infinite, and quotients can pass 127
+    x = torch.zeros(3, 64, dtype=torch.bfloat16)
+    for i, v in enumerate((2.0 ** -133, 2.0 ** -126, 2.0 ** -101)):
+        x[i] = torch.arange(-32, 32) / 32 * v
+    q, scale = i8.i8_quantize(x.cuda())
+    s = x.float().abs().amax(1) / 127
+    assert torch.equal(scale.cpu(), s)
+    want = torch.where(s[:, None] > 0, x.float() / s[:, None], torch.zeros(1)).round().clamp(-127, 127)
+    assert torch.equal(q.cpu().float(), want)
