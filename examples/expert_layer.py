@@ -2,8 +2,8 @@
 
     python examples/expert_layer.py
 
-Trains a small layer for a few steps (row grouping, grouped products and their
-gradients), then quantizes its experts to 4 bits and decodes a batch of tokens
+Trains a small layer for a few steps (routing, row grouping, grouped products and
+their gradients), then quantizes its experts to 4 bits and decodes a batch of tokens
 through them, one launch per projection, without grouping the rows.
 """
 import os
@@ -14,7 +14,7 @@ import torch
 if __name__ == "__main__":
     sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
-from dense_tiled_gemm_02_amd import grouped, w4
+from dense_tiled_gemm_02_amd import grouped, router, w4
 
 
 class ExpertLayer(torch.nn.Module):
@@ -30,8 +30,8 @@ class ExpertLayer(torch.nn.Module):
         self.down = init(experts, hidden, width)
 
     def route(self, x):
-        p, ids = torch.softmax((x @ self.router).float(), -1).topk(self.top)
-        return (p / p.sum(-1, keepdim=True)).to(x.dtype), ids
+        p, ids = router.route(x @ self.router, self.top)
+        return p.to(x.dtype), ids
 
     @staticmethod
     def act(h):
