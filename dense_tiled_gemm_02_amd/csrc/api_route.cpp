@@ -143,8 +143,6 @@ gemm_status gemm_route_grad(const gemm_route_problem* prob, const void* logits, 
     a.dl = dlogits;
     a.R = p.R;
     a.sl = p.sl;
-    a.sg = p.top;
-    a.sd = p.E;
     a.E = p.E;
     a.top = p.top;
     a.sigmoid = p.score == GEMM_SCORE_SIGMOID;

@@ -31,9 +31,9 @@ struct RouteArgs {
 struct RouteGradArgs {
     const void* logits;
     const int32_t* ids;    // R x top
-    const float* dw;       // R x top, rows sg elements apart
+    const float* dw;       // R x top
     void* dl;              // R x E, of the logits' type
-    int64_t R, sl, sg, sd;
+    int64_t R, sl;
     int64_t first;         // the launch's first row (filled in by launch_route_grad)
     int32_t E, top;
     int32_t sigmoid, renorm;

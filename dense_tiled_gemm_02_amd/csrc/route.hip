@@ -491,7 +491,6 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
     sort_keys<J>(key);
     uint32_t before = 0;
     int n = 0;   // ids so far: `top` of them, or more where those after the last are close to it
-    bool all = true;
     for (; n < kMaxTop; ++n) {
         const uint32_t m = lanes<LANES>(key[0], MaxU());
         if (m == 0) break;
@@ -513,13 +512,19 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
         for (int j = 0; j + 1 < J; ++j) key[j] = (key[j + 1] & moved) | (key[j] & ~moved);
         key[J - 1] &= ~moved;
         before = m;
-        all = n + 1 < kMaxTop;   // false: there may be more that are close
+    }
+    bool all = true;   // that are close to one another are in ids
+    if constexpr (SCORED || !WHOLE) {
+        if (n == kMaxTop) {
+            const uint32_t m = lanes<LANES>(key[0], MaxU());
+            all = m == 0 || value_of(before) - value_of(m) > far;
+        }
     }
     for (int k = n + lane; k < a.top; k += LANES) ids[k] = -1;
     if constexpr (SCORED || !WHOLE) {
-        if (__builtin_expect(close, 0)) {
+        if (__builtin_expect(close | !all, 0)) {
             wave_lds_fence();
-            if (all || far < 0) exact.rank(shared, ids, n, biased);
+            if (all) exact.rank(shared, ids, n, biased);
             else exact.choose(shared, ids, biased, kept);
         }
     }
@@ -616,7 +621,7 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouteGradArgs a) {
         id[i] = t < a.top ? a.ids[row * a.top + t] : -1;
         if (id[i] >= a.E) id[i] = -1;
         cl[i] = id[i] >= 0 ? logit<KIND>(a.logits, row * a.sl + id[i]) : -kInf;
-        g[i] = id[i] >= 0 ? a.dw[row * a.sg + t] * a.scale : 0.0f;
+        g[i] = id[i] >= 0 ? a.dw[row * a.top + t] * a.scale : 0.0f;
         most = fmaxf(most, cl[i]);
     }
     if (renorm) most = row_max<LANES>(most);
@@ -654,7 +659,7 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouteGradArgs a) {
         for (int j = 0; j < J; ++j)
             if (j == e) out[j] += d;
     }
-    store_logits<J, KIND>(a.dl, row * a.sd, e0, a.E, out);
+    store_logits<J, KIND>(a.dl, row * a.E, e0, a.E, out);
 }
 
 // Rows of a launch: of more, several follow one another.

@@ -309,3 +309,18 @@ def test_calls_made_twice():
                dict(scale=float("nan")), dict(top=-1)):
         with pytest.raises(RuntimeError):
             router.route(l, **{"top": 3, **kw})
+
+
+def test_the_last_of_as_many_choices_as_there_can_be():
+    """The 64th and the 65th differ by less than fp32 keys tell apart, the larger one behind."""
+    for E in (100, 200, 300, 1024):
+        l = torch.empty(40, E)
+        l[:] = -torch.arange(E) / 50
+        l[:, 1:64] = 10 + torch.arange(63) / 10
+        for row in range(40):
+            l[row, 0] = 5 + row * 37 * 2.0 ** -21
+            l[row, E - 9] = l[row, 0] + 2.0 ** -20
+        for score in ("softmax", "sigmoid"):
+            for bias in (None, torch.zeros(E)):
+                ids = check(l, 64, score=score, bias=bias)
+                assert bool((ids[:, 63] == E - 9).all())
