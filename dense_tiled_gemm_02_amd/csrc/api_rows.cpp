@@ -67,7 +67,8 @@ gemm_status sizes(int64_t R, int64_t K, gemm_dtype dtype, const Stride* s, int n
     if (R < 0 || K < 0) return fail(GEMM_ERR_INVALID_ARG, "negative size R=%lld K=%lld", (long long)R, (long long)K);
     if (dtype != GEMM_F16 && dtype != GEMM_BF16)
         return fail(GEMM_ERR_INVALID_ARG, "dtype %d: rows are GEMM_F16 or GEMM_BF16", (int)dtype);
-    if (R > dtg::kMaxSize || K > dtg::kMaxSize) return fail(GEMM_ERR_UNSUPPORTED, "sizes above 2^31-4096 are not supported");
+    if (R > dtg::kMaxSize || K > dtg::kMaxRow)
+        return fail(GEMM_ERR_UNSUPPORTED, "more than 2^31-4096 rows or 2^24 values a row are not supported");
     for (int i = 0; i < n; ++i) {
         if (s[i].stride < 0) return fail(GEMM_ERR_UNSUPPORTED, "negative stride of %s", s[i].name);
         if (extent(R, s[i].stride, K, 4) < 0) return fail(GEMM_ERR_INVALID_ARG, "the stride of %s reaches past 2^60 bytes", s[i].name);

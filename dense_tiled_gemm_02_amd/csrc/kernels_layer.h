@@ -7,6 +7,8 @@
 
 namespace dtg {
 
+constexpr int64_t kMaxRow = int64_t(1) << 24;   // K
+
 // One row each: h = x (+ r), y = h w / sqrt(mean h^2 + eps) (w nullptr: y = x),
 // as 16-bit values (y) or as int8 with the row's scale (q).  Strides in
 // elements; rows of K contiguous elements at any address.

@@ -10,7 +10,8 @@
 // bits), with the sums across them through the wave's lanes and, where a row
 // takes more than a wave, one LDS word per wave and one barrier.  Bound by memory:
 // x, r are read and y or q (and h) are written once.  Rows longer than the
-// registers hold are read again for each pass (C = 0).
+// registers hold are read again for each pass (C = 0); kMaxRow keeps their sums
+// (a chunk's 8, then up to 2048 chunks a thread, in a row) within 2^-13.
 //
 // The quotient y / s is defined as an IEEE division by the stored scale, rounded
 // to the nearest integer; see steps_of for how most of it is done without one.
@@ -146,8 +147,8 @@ __device__ __forceinline__ void weights8(const void* w, int w32, int k, int K, f
     }
 }
 
-// 1 / sqrt(sum / K + eps).  A sum of squares that overflows (bf16 values past
-// 1e19) is taken again, scaled by 2^-200.
+// A sum of squares that overflows (bf16 values past 1e19) is taken again, of the
+// values scaled by this.
 constexpr float kSmaller = 0x1p-100f;
 
 // Eight quotients v / s as bytes.  v times the reciprocal of s, added to 1.5 x 2^23,
@@ -251,17 +252,20 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rows_kernel(RowsArgs a) {
                     float v[8];
                     widen8<BF16>(u, v);
                     const int skip = C > 0 && odd ? k - from(k) : 0;
+                    float part = 0.0f;   // a chunk by itself: a long row's sum is not rounded for every value
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float w = (C > 0 && odd && e < skip ? 0.0f : v[e]) * by;
-                        ss = fmaf(w, w, ss);
+                        part = fmaf(w, w, part);
                     }
+                    ss += part;
                 });
                 return meet.sum(ss);
             };
             const float ss = squares(false, 1.0f);
             // rows of one wave meet by lanes alone; of several, every thread of the workgroup is here
-            if (BF16 && __builtin_expect(ss == kInf, 0)) rstd = kSmaller / sqrtf(squares(true, kSmaller) / static_cast<float>(K));
+            if (BF16 && __builtin_expect(ss == kInf, 0))
+                rstd = kSmaller / sqrtf(squares(true, kSmaller) / static_cast<float>(K) + a.eps * kSmaller * kSmaller);
             else rstd = 1.0f / sqrtf(ss / static_cast<float>(K) + a.eps);
             if (a.rstd && live && t == 0) a.rstd[row] = rstd;
         }
@@ -397,8 +401,10 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_grad_kernel(NormGradAr
             for (int k = 8 * t; k < Kr; k += 8 * T) {
                 float g[8], u[8], wk[8];
                 both(k, g, u, wk);
+                float part = 0.0f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) dot = fmaf(g[e] * wk[e], u[e], dot);
+                for (int e = 0; e < 8; ++e) part = fmaf(g[e] * wk[e], u[e], part);
+                dot += part;
             }
             const float mean = meet.sum(dot) / count;
             for (int k = 8 * t; k < Kr; k += 8 * T) {

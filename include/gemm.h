@@ -437,7 +437,7 @@ gemm_status gemm_w4_run(const gemm_w4_plan* plan, const void* X, const void* W, 
  * bitwise reproducible.  No outputs may overlap anything.  rstd: NULL, or R
  * floats that receive 1 / n for the gradient.  No workspace; capturable. */
 typedef struct gemm_norm_problem {
-    int64_t R, K;               /* each up to 2^31 - 4096 */
+    int64_t R, K;               /* up to 2^31 - 4096 rows of up to 2^24 */
     int64_t sx, sr;             /* row strides in elements: x and r, */
     int64_t sh, sy;             /* h, and y or q (gradient: see there) */
     gemm_dtype dtype;           /* of the rows: GEMM_F16 or GEMM_BF16 */

@@ -363,3 +363,40 @@ def test_quotients_halfway_between_two_steps():
     assert torch.equal(scale.cpu(), s)
     want = torch.where(s[:, None] > 0, x.float() / s[:, None], torch.zeros(1)).round().clamp(-127, 127)
     assert torch.equal(q.cpu().float(), want)
+
+
+@pytest.mark.parametrize("K", [(1 << 20) + 3, 1 << 24])
+def test_long_rows(K):
+    """In fp32 a sum of K values of one sign goes through K / 8192 + 8 + 26 additions in a row: a thread's
+    chunks, a chunk's values, the threads and the waves."""
+    fp32 = (K / 8192 + 40) * 2.0 ** -24
+    x, dy = rows(2, K, torch.bfloat16, 1), rows(2, K, torch.bfloat16, 2)
+    w = rows(1, K, torch.float32, 3)[0]
+    dx_w = [t.cuda().requires_grad_() for t in (x, w)]
+    y = norm.rms_norm(*dx_w, eps=EPS)
+    u = half_step(torch.bfloat16)
+    x64, w64, dy64 = x.double(), w.double(), dy.double()
+    rstd = 1 / torch.sqrt(x64.square().mean(1, keepdim=True) + EPS)
+    want = x64 * w64 * rstd
+    near(y.detach(), want, want.abs() * (u + fp32) + smallest(torch.bfloat16), "y")
+    q, scale = norm.rms_norm_i8(dx_w[0].detach(), dx_w[1].detach(), eps=EPS)
+    most = want.abs().amax(1)
+    near(scale, most / 127, most / 127 * (fp32 + 2.0 ** -20), "scale")
+    near(q.cpu().double() * scale.cpu().double()[:, None], want, (most / 127 * 0.5)[:, None] + want.abs() * (fp32 + 2.0 ** -20), "q")
+    dx, dw = torch.autograd.grad(y, dx_w, dy.cuda())
+    g, v = dy64 * w64, x64 * rstd
+    mean, off = (g * v).mean(1, keepdim=True), (g * v).abs().mean(1, keepdim=True)
+    want = (g - v * mean) * rstd
+    bound = want.abs() * (u + fp32) + ((g.abs() + v.abs() * mean.abs()) * (fp32 + 2.0 ** -21) + v.abs() * off * fp32) * rstd
+    near(dx, want, bound + smallest(torch.bfloat16), "dx")
+    near(dw, (dy64 * v).sum(0), (dy64 * v).abs().sum(0) * (fp32 + 2.0 ** -21), "dw")
+
+
+def test_eps_counts_where_the_squares_overflow():
+    """Values and eps near the largest: 1 / sqrt(mean + eps) of a mean past fp32's range."""
+    x = torch.full((3, 40), 2.0 ** 64, dtype=torch.bfloat16)
+    x[1] *= 2
+    w = torch.ones(40, dtype=torch.bfloat16)
+    y = norm.rms_norm(x.cuda(), w.cuda(), eps=3e38)
+    want = x.double() / torch.sqrt(x.double().square().mean(1, keepdim=True) + 3e38)
+    near(y, want, want * (half_step(torch.bfloat16) + FP32), "y")

@@ -146,3 +146,11 @@ def test_the_formula_against_differences():
                 u[at] += s
                 ends.append(value(u.view_as(t), w) if t is h else value(h, u))
             assert abs((ends[0] - ends[1]) / (2 * step) - d.reshape(-1)[at]) < 1e-8
+
+
+def test_rows_too_long_for_their_sums_are_refused():
+    longest = 1 << 24
+    refused(UNSUPPORTED, lambda: norm.gemm_rms_norm(problem(K=longest + 1), A, A, A, A, A, None))
+    refused(UNSUPPORTED, lambda: norm.gemm_rms_norm_grad_workspace(problem(K=longest + 1)))
+    refused(UNSUPPORTED, lambda: i8.gemm_i8_quantize(A, g.GEMM_BF16, 1, longest + 1, longest + 1, A, longest + 1, A))
+    assert norm.gemm_rms_norm_grad_workspace(problem(K=longest)) > 0
