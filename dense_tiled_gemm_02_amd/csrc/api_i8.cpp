@@ -74,7 +74,9 @@ bool chunked(const gemm_i8_problem* p) {
 }
 
 // 32-bit offsets of `rows` rows from a rebased descriptor.
-bool near(int64_t rows, int64_t stride, int64_t K) { return rows * stride + K < (int64_t(1) << 31) - 4096; }
+bool near(int64_t rows, int64_t stride, int64_t K) {
+    return stride < (int64_t(1) << 31) && rows * stride + K < (int64_t(1) << 31) - 4096;
+}
 
 // The smallest tile of at most 64 x 32 whose workgroups the CUs hold at once: K is
 // long beside the tile, and its waves share it out, so that a second round or a

@@ -103,3 +103,11 @@ def test_torch_calls_refuse_by_name():
                           (TypeError, dict(out=torch.zeros(3, 5, dtype=torch.int32))), (ValueError, {})]:
         with pytest.raises(error):
             i8.i8_matmul(**{**good, **change})
+
+
+def test_strides_past_any_memory_take_no_offsets_of_32_bits():
+    for M, N, K in ((2, 2, 4096), (300, 2, 4096)):
+        for change in (dict(sx=1 << 59), dict(sw=1 << 59), dict(sx=1 << 56), dict(sw=1 << 56)):
+            if M > 16 and "sx" in change:
+                continue   # reaches past 2^60
+            assert "i8_any_kernel" in plan(M=M, N=N, K=K, **{"sx": K, "sw": K, "sy": N, **change}).describe()
