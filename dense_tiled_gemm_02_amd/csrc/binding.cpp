@@ -28,11 +28,14 @@
 #include <Python.h>
 #include <ATen/ATen.h>
 #include <c10/hip/HIPFunctions.h>
+#include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/autograd/variable.h>
 
+#include <algorithm>
 #include <cstring>
 #include <unordered_map>
 #include <utility>
@@ -318,10 +321,30 @@ struct NormFunction : torch::autograd::Function<NormFunction> {
 
 bool wants_grad(const at::Tensor& t) { return t.defined() && t.requires_grad(); }
 
+// A leaf's gradient is collected on the stream that its first live graph was
+// recorded on.  Where that is not the stream of a capture, the captured backward
+// pass would draw the other stream into the capture, and the process ends.
+void one_stream(const at::Tensor& leaf, const char* what) {
+    if (!wants_grad(leaf) || !leaf.is_leaf()) return;
+    const auto collector = torch::autograd::impl::try_get_grad_accumulator(leaf);
+    if (!collector) return;
+    const auto stream = collector->stream();
+    const c10::Stream now = c10::hip::getCurrentHIPStream(leaf.device().index()).unwrap();
+    if (stream && stream->id() != now.id())
+        throw std::runtime_error(std::string(what) + ": in a graph's capture, while a graph of the same leaf recorded on another "
+                                 "stream is alive; let go of that one first (its outputs, too), or record it on the capture's stream");
+}
+void capturable(const at::Tensor& a, const at::Tensor& b, const at::Tensor& c, const char* what) {
+    if (c10::hip::currentStreamCaptureStatusMayInitCtx() == c10::hip::CaptureStatus::None) return;
+    for (const at::Tensor* t : {&a, &b, &c}) one_stream(*t, what);
+}
+
 // The outputs of an operator, in order.
 variable_list norm_call(const at::Tensor& x, const at::Tensor& w, const at::Tensor& r, double eps) {
-    if (at::GradMode::is_enabled() && (wants_grad(x) || wants_grad(w) || wants_grad(r)))
+    if (at::GradMode::is_enabled() && (wants_grad(x) || wants_grad(w) || wants_grad(r))) {
+        capturable(x, w, r, "rms_norm");
         return NormFunction::apply(x, w, r.defined() ? std::optional<at::Tensor>(r) : std::nullopt, eps);
+    }
     const Normed n = norm_rows(x, w, r, eps, false);
     if (n.h.defined()) return {n.y, n.h};
     return {n.y};
@@ -354,7 +377,7 @@ struct RouteParameters {
 gemm_route_problem route_problem(const at::Tensor& logits, bool bias, const RouteParameters& a) {
     gemm_route_problem p = {};
     p.R = logits.size(0);
-    p.E = static_cast<int32_t>(logits.size(1));
+    p.E = static_cast<int32_t>(std::min<int64_t>(logits.size(1), INT32_MAX));
     p.sl = logits.stride(0);
     p.top = static_cast<int32_t>(a.v[0]);
     p.score = static_cast<gemm_score>(a.v[1]);
@@ -369,7 +392,8 @@ gemm_route_problem route_problem(const at::Tensor& logits, bool bias, const Rout
 }
 
 variable_list route_rows(const at::Tensor& logits, const at::Tensor& bias, const RouteParameters& a) {
-    at::Tensor w = make({logits.size(0), a.v[0]}, at::kFloat, logits), ids = make({logits.size(0), a.v[0]}, at::kInt, logits);
+    const int64_t top = a.v[0] >= 0 && a.v[0] <= logits.size(1) ? a.v[0] : 0;   // others are refused
+    at::Tensor w = make({logits.size(0), top}, at::kFloat, logits), ids = make({logits.size(0), top}, at::kInt, logits);
     const gemm_route_problem p = route_problem(logits, bias.defined(), a);
     check(library.route(&p, data(logits), static_cast<const float*>(data(bias)), static_cast<float*>(data(w)),
                         static_cast<int32_t*>(data(ids)), stream_of(logits)));
@@ -410,9 +434,11 @@ struct RouteFunction : torch::autograd::Function<RouteFunction> {
 };
 
 variable_list route_call(const at::Tensor& logits, const at::Tensor& bias, const RouteParameters& a) {
-    if (at::GradMode::is_enabled() && wants_grad(logits))
+    if (at::GradMode::is_enabled() && wants_grad(logits)) {
+        capturable(logits, at::Tensor(), at::Tensor(), "route");
         return RouteFunction::apply(logits, bias.defined() ? std::optional<at::Tensor>(bias) : std::nullopt,
                                     std::vector<int64_t>(a.v, a.v + kRouteInts), a.scale);
+    }
     return route_rows(logits, bias, a);
 }
 

@@ -110,8 +110,9 @@ def rms_norm(x, weight, residual=None, eps=1e-6, stream=None):
 
     x, residual: R x K, float16 or bfloat16, unit stride along the rows; weight: K
     values of that type or float32.  Sums in float32, y rounded once.
-    Differentiable (once).  Asynchronous on `stream` (default: torch's current
-    stream)."""
+    Differentiable (once); in a graph's capture that is refused while another
+    stream's graph of the same leaf is alive.  Asynchronous on `stream` (default:
+    torch's current stream)."""
     eps = float(eps)
     if stream is None:
         out = _remembered(NORM, eps, x, weight, residual)

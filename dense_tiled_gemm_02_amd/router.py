@@ -51,8 +51,9 @@ def route(logits, top, score="softmax", bias=None, groups=1, top_groups=1, group
     part (strength: the sum of a group's best group_best, 1 or 2, scores with
     bias).  Equal scores: the lowest index first.  An expert with a logit or bias
     of -inf or NaN is never chosen; ids that are left over are -1 with weight 0.
-    The weights are differentiable (once) for the logits.  Asynchronous on
-    `stream` (default: torch's current stream)."""
+    The weights are differentiable (once) for the logits; in a graph's capture that
+    is refused while another stream's graph of the same leaf is alive.  Asynchronous
+    on `stream` (default: torch's current stream)."""
     how = (top, SCORES.get(score, -1), groups, top_groups, group_best, 1 if renormalize else 0, float(scale))
     if stream is None:
         pair = _remembered(ROUTE, how, logits, bias)
@@ -83,7 +84,8 @@ def route_grad(dweights, logits, ids, score="softmax", renormalize=True, scale=1
     def call():
         dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
         p = gemm_route_problem()
-        p.R, p.E, p.top, p.sl = logits.shape[0], logits.shape[1], ids.shape[1], logits.stride(0)
+        most = 2 ** 31 - 1   # of the fields; refused
+        p.R, p.E, p.top, p.sl = logits.shape[0], min(logits.shape[1], most), min(ids.shape[1], most), logits.stride(0)
         p.groups = p.top_groups = p.group_best = 1
         p.renormalize, p.scale = 1 if renormalize else 0, scale
         p.dtype, p.score = _CODES[logits.dtype], SCORES[score]

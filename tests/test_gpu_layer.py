@@ -152,3 +152,44 @@ def test_decoding_step_eager_and_captured(R):
         close(after, want_after, 3 * Q + 7 * U, "stream")
         close(got, want, 3 * Q + 12 * U, "output")
         x, stream = got, after
+
+
+def test_capture_next_to_a_live_graph_of_the_same_leaves_is_refused():
+    """The captured backward pass would wait on the live graph's stream, which ends the process."""
+    x, logits = (torch.randn(8, 64, dtype=BF16, device="cuda", requires_grad=True) for _ in range(2))
+    weight = torch.ones(64, device="cuda", requires_grad=True)
+    alive = norm.rms_norm(x, weight), router.route(logits, 2)
+    calls = (lambda: norm.rms_norm(x, weight.detach()), lambda: norm.rms_norm(x.detach(), weight),
+             lambda: norm.rms_norm(x.detach(), weight.detach(), x), lambda: router.route(logits, 2))
+    torch.cuda.synchronize()
+    for call in calls:
+        call()   # not in a capture
+    out = torch.zeros(4, device="cuda")
+    graph, refusals = torch.cuda.CUDAGraph(), []
+    with torch.cuda.graph(graph):
+        out += 1
+        for call in calls:
+            try:
+                call()
+            except RuntimeError as e:
+                refusals.append(str(e))
+        with torch.no_grad():   # no gradient, no collector
+            norm.rms_norm(x, weight)
+    assert len(refusals) == len(calls) and all("another stream is alive" in r for r in refusals)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert out.tolist() == [1, 1, 1, 1]
+    del alive
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = norm.rms_norm(x, weight)
+        w, _ = router.route(logits, 2)
+        grads = torch.autograd.grad((y, w), (x, weight, logits), (torch.ones_like(y), torch.ones_like(w)))
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    got = [g.clone() for g in grads]
+    del y, w, grads
+    y, (w, _) = norm.rms_norm(x, weight), router.route(logits, 2)
+    for a, b in zip(got, torch.autograd.grad((y, w), (x, weight, logits), (torch.ones_like(y), torch.ones_like(w)))):
+        assert torch.equal(a, b)
