@@ -7,6 +7,7 @@ magnitude / 254: rows of normal values have their largest within 5 times their
 root mean square, so 5 / 254 of the row's norm (Q)."""
 import importlib.util
 import os
+import threading
 
 import pytest
 import torch
@@ -193,3 +194,36 @@ def test_capture_next_to_a_live_graph_of_the_same_leaves_is_refused():
     y, (w, _) = norm.rms_norm(x, weight), router.route(logits, 2)
     for a, b in zip(got, torch.autograd.grad((y, w), (x, weight, logits), (torch.ones_like(y), torch.ones_like(w)))):
         assert torch.equal(a, b)
+
+
+def test_threads_with_streams_of_their_own():
+    """New sizes and known ones, forward and backward, from several threads at once: each result as alone."""
+    def work(seed):
+        out = []
+        for turn in range(12):
+            R, K, E = 1 + (7 * seed + turn) % 5, 64 * (1 + turn % 4), 8 * (1 + (seed + turn) % 3)
+            gen = torch.Generator().manual_seed(100 * seed + turn)
+            x, w, r = (torch.randn(s, generator=gen).to(BF16).cuda().requires_grad_() for s in ((R, K), (K,), (R, E)))
+            y, h = norm.rms_norm(x, w, x)
+            p, ids = router.route(r, 2)
+            q, scale = i8.i8_quantize(y.detach())
+            v, steps = i8.i8_quantize(torch.randn(48, K, generator=gen).to(BF16).cuda())
+            out += [y, h, p, ids, i8.i8_matmul(q, scale, v, steps)]
+            out += torch.autograd.grad((y, p), (x, w, r), (torch.ones_like(y), p.detach()))
+        torch.cuda.current_stream().synchronize()
+        return [t.detach().cpu() for t in out]
+
+    def thread(seed):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            results[seed] = work(seed)
+
+    results = {}
+    threads = [threading.Thread(target=thread, args=(seed,)) for seed in range(6)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(results) == len(threads)
+    for seed, got in results.items():
+        for a, b in zip(got, work(seed)):
+            assert torch.equal(a, b)
