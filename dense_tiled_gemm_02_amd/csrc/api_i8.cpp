@@ -144,6 +144,7 @@ gemm_status plan_impl(const gemm_i8_problem* given, const gemm_device_info* dev,
     pl->prob = *p;
     pl->out = p->out == GEMM_F32 ? dtg::kOutF32 : p->out == GEMM_BF16 ? dtg::kOutBF16 : dtg::kOutF16;
     pl->cus = dev->cu_count;
+    pl->xcds = dev->xcd_count > 0 ? dev->xcd_count : 1;
     if (chunked(p)) {
         pl->few = pick_few(p, dev);
         if (!pl->few) pl->tile = pick_tile(p, dev, pl->out);
@@ -152,10 +153,10 @@ gemm_status plan_impl(const gemm_i8_problem* given, const gemm_device_info* dev,
         pl->tiles_m = cdiv(p->M, pl->tile->bm);
         pl->tiles_n = cdiv(p->N, pl->tile->bn);
         pl->group_m = 8;
-        pl->xcds = dev->xcd_count > 0 ? dev->xcd_count : 1;
     } else {
-        pl->tiles_m = cdiv(p->M, pl->few ? 16 * pl->few->mb : 64);
-        pl->tiles_n = cdiv(p->N, pl->few ? 16 * pl->few->nb : 64);
+        const int side = dtg::i8_any_tile(p->M, p->N, pl->cus);
+        pl->tiles_m = cdiv(p->M, pl->few ? 16 * pl->few->mb : side);
+        pl->tiles_n = cdiv(p->N, pl->few ? 16 * pl->few->nb : side);
     }
     *out = pl;
     return GEMM_OK;
@@ -253,7 +254,7 @@ gemm_status gemm_i8_run(const gemm_i8_plan* plan, const int8_t* X, const float* 
         a.lx = p.sx;
         a.lw = p.sw;
         a.ly = p.sy;
-        err = plan->few && aligned ? plan->few->launch[plan->out](a, on) : dtg::launch_i8_any(a, plan->out, plan->cus, on);
+        err = plan->few && aligned ? plan->few->launch[plan->out](a, on) : dtg::launch_i8_any(a, plan->out, plan->cus, plan->xcds, on);
     }
     return err == hipSuccess ? GEMM_OK : fail(GEMM_ERR_HIP, "launch of the int8 product: %s", hipGetErrorString(err));
 }

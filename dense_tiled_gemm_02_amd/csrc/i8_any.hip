@@ -2,23 +2,25 @@
 // direct-to-LDS kernels do not take: K, row strides or bases that are no
 // multiples of 16 bytes.
 //
-// 64 x 64 outputs to a workgroup, 128 k a step.  Every chunk of 16 k is one load
+// 64 x 64 or 128 x 128 outputs to a workgroup, 128 k a step.  Every chunk of 16 k is one load
 // at its own address, whatever that is, through registers one step ahead into one
-// of two LDS stages.  Rows past the operands read the last row, and what they make is not stored.  Bound by the
-// latency of a step, not by bytes, so where the tiles are at most one to a CU KG
-// groups of four waves take the steps in turn, each with its own stages, and
-// their sums meet in LDS.  The sums are exact (int32), so nothing depends on
-// their order.
+// of two LDS stages.  Rows past the operands read the last row, and what they make
+// is not stored.  Where the tiles are at most one to a CU KG groups of four waves
+// take the steps in turn, each with its own stages, and their sums meet in LDS.
+// The sums are exact (int32), so nothing depends on their order.
 //
-// 777 x 1003 x 2005, rows at any byte, 13.1 us; rows of whole words 9.7 us (loads at
-// other addresses take longer; whole words around them, shifted, 12.2 and 12.3).
-// Two or three steps ahead: 13.5 and 14.8 us.
+// Bound by the loads of single bytes' alignment, which take a CU 49 cycles each
+// where aligned ones take 26 (512 k of a tile 1.5 and 0.8 us): 777 x 1003 x 2005 12.0
+// us, with rows of whole words 10.3.  Whole words around each chunk, shifted in
+// registers, cost as much (12.2, and 12.3 for whole words).  Two or three steps
+// ahead: 1.03 and 1.13 times the time of one.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include "device_common.h"
 #include "i8_epilogue.h"
 #include "kernels_i8.h"
+#include "tile_order.h"
 
 namespace dtg {
 namespace {
@@ -29,20 +31,32 @@ struct __attribute__((packed, aligned(1))) Loose16 {
     u32x4 v;
 };
 
-constexpr int kTile = 64, kStep = 128, kThreads = 256;
-constexpr int kChunks = kStep / 16;                                // to a row
-constexpr int kLoads = kTile * kChunks / kThreads;                 // of an operand, to a thread
-constexpr int kStage = kTile * kStep;                              // bytes of an operand
+constexpr int kStep = 128, kThreads = 256;
+constexpr int kChunks = kStep / 16;   // to a row
 
-template <int KG, int OUT>
-__global__ __launch_bounds__(KG * kThreads) void i8_any_kernel(I8RowsArgs a, int tiles_n) {
+// Where a workgroup's tile lies (tile_order.h): a die's tiles next to one another,
+// in bands of kBand rows of tiles (4096 x 4097 x 4095 of equal values, 64 x 64 tiles:
+// 183 us in plain order, bands of 1, 4, 8, 16 rows 171, 136, 131, 139).
+constexpr int kBand = 8;
+struct Order {
+    int tiles_m, tiles_n, group_m, xcds;
+};
+
+// Tiles of 32 TB rows and columns; a wave has TB x TB blocks of 16 x 16.
+template <int TB, int KG, int OUT>
+__global__ __launch_bounds__(KG * kThreads) void i8_any_kernel(I8RowsArgs a, Order order) {
+    constexpr int kTile = 32 * TB;
+    constexpr int kLoads = kTile * kChunks / kThreads;   // of an operand, to a thread
+    constexpr int kStage = kTile * kStep;                // bytes of an operand
+    static_assert(KG == 1 || TB == 2, "the groups' sums are four blocks a wave");
     __shared__ __attribute__((aligned(16))) uint8_t all[KG * 2 * 2 * kStage];
     const int group = threadIdx.x / kThreads;   // whole waves
     const int tid = threadIdx.x % kThreads, lane = tid & 63, wave = tid >> 6;
     uint8_t* const smem = all + group * 2 * 2 * kStage;
     const int wm = wave >> 1, wn = wave & 1;
-    const int64_t tile = blockIdx.x;
-    const int m0 = static_cast<int>(tile / tiles_n) * kTile, n0 = static_cast<int>(tile % tiles_n) * kTile;
+    int pm, pn;
+    grouped_tile<int>(xcd_permute<int>(blockIdx.x, gridDim.x, order.xcds), order.tiles_m, order.tiles_n, order.group_m, &pm, &pn);
+    const int m0 = pm * kTile, n0 = pn * kTile;
     const int K = a.K;
 
     const int8_t* src[2][kLoads];
@@ -105,11 +119,11 @@ __global__ __launch_bounds__(KG * kThreads) void i8_any_kernel(I8RowsArgs a, int
             }
     };
 
-    f32x4 acc[2][2];   // int32 bits; [m block][n block], a lane: one m, four n
+    f32x4 acc[TB][TB];   // int32 bits; [m block][n block], a lane: one m, four n
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < TB; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < TB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
     // of every group as many: steps past K are zeros
     const int steps = ((K + kStep - 1) / kStep + KG - 1) / KG;
@@ -121,17 +135,17 @@ __global__ __launch_bounds__(KG * kThreads) void i8_any_kernel(I8RowsArgs a, int
         const uint8_t *x = smem + 2 * (s & 1) * kStage, *w = x + kStage;
 #pragma unroll
         for (int ks = 0; ks < kStep / 64; ++ks) {
-            u32x4 fx[2], fw[2];
+            u32x4 fx[TB], fw[TB];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int c = 4 * ks + (lane >> 4), rx = wm * 32 + i * 16 + (lane & 15), rw = wn * 32 + i * 16 + (lane & 15);
+            for (int i = 0; i < TB; ++i) {
+                const int c = 4 * ks + (lane >> 4), rx = (wm * TB + i) * 16 + (lane & 15), rw = (wn * TB + i) * 16 + (lane & 15);
                 fx[i] = *reinterpret_cast<const u32x4*>(x + rx * kStep + 16 * (c ^ swz<kChunks>(rx)));
                 fw[i] = *reinterpret_cast<const u32x4*>(w + rw * kStep + 16 * (c ^ swz<kChunks>(rw)));
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < TB; ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) acc[i][j] = mfma_i8<16>(fw[j], fx[i], acc[i][j]);
+                for (int j = 0; j < TB; ++j) acc[i][j] = mfma_i8<16>(fw[j], fx[i], acc[i][j]);
         }
     }
     if constexpr (KG > 1) {
@@ -153,30 +167,44 @@ __global__ __launch_bounds__(KG * kThreads) void i8_any_kernel(I8RowsArgs a, int
         }
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int m = m0 + wm * 32 + i * 16 + (lane & 15);
+    for (int i = 0; i < TB; ++i) {
+        const int m = m0 + (wm * TB + i) * 16 + (lane & 15);
         if (m >= a.M) continue;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            store_scaled<OUT>(a, m, n0 + wn * 32 + j * 16 + 4 * (lane >> 4), acc[i][j]);
+        for (int j = 0; j < TB; ++j)
+            store_scaled<OUT>(a, m, n0 + (wn * TB + j) * 16 + 4 * (lane >> 4), acc[i][j]);
     }
 }
 
-template <int KG>
-hipError_t launch(const I8RowsArgs& a, int out, int tiles, int tiles_n, hipStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(tiles)), block(KG * kThreads);
-    if (out == kOutF32) hipLaunchKernelGGL((i8_any_kernel<KG, kOutF32>), grid, block, 0, stream, a, tiles_n);
-    else if (out == kOutBF16) hipLaunchKernelGGL((i8_any_kernel<KG, kOutBF16>), grid, block, 0, stream, a, tiles_n);
-    else hipLaunchKernelGGL((i8_any_kernel<KG, kOutF16>), grid, block, 0, stream, a, tiles_n);
+template <int TB, int KG>
+hipError_t launch(const I8RowsArgs& a, int out, int xcds, hipStream_t stream) {
+    const Order order = {static_cast<int>((static_cast<int64_t>(a.M) + 32 * TB - 1) / (32 * TB)),
+                         static_cast<int>((static_cast<int64_t>(a.N) + 32 * TB - 1) / (32 * TB)), kBand, xcds};
+    const dim3 grid(static_cast<unsigned>(order.tiles_m) * order.tiles_n), block(KG * kThreads);
+    if (out == kOutF32) hipLaunchKernelGGL((i8_any_kernel<TB, KG, kOutF32>), grid, block, 0, stream, a, order);
+    else if (out == kOutBF16) hipLaunchKernelGGL((i8_any_kernel<TB, KG, kOutBF16>), grid, block, 0, stream, a, order);
+    else hipLaunchKernelGGL((i8_any_kernel<TB, KG, kOutF16>), grid, block, 0, stream, a, order);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_i8_any(const I8RowsArgs& a, int out, int cus, hipStream_t stream) {
-    const int64_t tm = (static_cast<int64_t>(a.M) + kTile - 1) / kTile, tn = (static_cast<int64_t>(a.N) + kTile - 1) / kTile;
-    if (tm * tn <= cus) return launch<4>(a, out, static_cast<int>(tm * tn), static_cast<int>(tn), stream);
-    return launch<1>(a, out, static_cast<int>(tm * tn), static_cast<int>(tn), stream);
+// us of 64 x 64 tiles with four groups and with one, and of 128 x 128, rows at any byte:
+//   1000 x 1000 x 1000   8.5, 8.2, 18.9   (256 of the small tiles, 64 of the large)
+//   777 x 1003 x 2005    12.6, 13.8, 30   (208, 56)
+//   300 x 4097 x 4095    36, 29, 47       (325, 99)
+//   20000 x 100 x 4095   51, 42.5, 44.9   (626, 157)
+//   128 x 28001 x 4095   88, 78, 54       (876, 219)
+//   4096 x 4097 x 4095   280, 220, 176    (4160, 1056)
+//   5000 x 5000 x 300    132, 52, 57      (6241, 1600)
+int i8_any_tile(int64_t M, int64_t N, int cus) {
+    return 4 * ((M + 127) / 128) * ((N + 127) / 128) < 3 * static_cast<int64_t>(cus) ? 64 : 128;
+}
+
+hipError_t launch_i8_any(const I8RowsArgs& a, int out, int cus, int xcds, hipStream_t stream) {
+    if (i8_any_tile(a.M, a.N, cus) == 128) return launch<4, 1>(a, out, xcds, stream);
+    const int64_t tiles = (static_cast<int64_t>(a.M) + 63) / 64 * ((static_cast<int64_t>(a.N) + 63) / 64);
+    return tiles <= cus ? launch<2, 4>(a, out, xcds, stream) : launch<2, 1>(a, out, xcds, stream);
 }
 
 }  // namespace dtg

@@ -53,7 +53,8 @@ struct I8FewEntry {
 };
 const I8FewEntry* i8_few_table(int* count);
 
-// Sizes, strides and addresses of any kind.
-hipError_t launch_i8_any(const I8RowsArgs& a, int out, int cus, hipStream_t stream);
+// Sizes, strides and addresses of any kind, in square tiles of i8_any_tile.
+int i8_any_tile(int64_t M, int64_t N, int cus);
+hipError_t launch_i8_any(const I8RowsArgs& a, int out, int cus, int xcds, hipStream_t stream);
 
 }  // namespace dtg

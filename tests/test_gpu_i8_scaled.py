@@ -174,3 +174,11 @@ def test_streams_and_graphs():
         got = [t.clone() for t in captured]
         for a, c in zip(got, step()):
             assert torch.equal(a, c)
+
+
+@pytest.mark.parametrize("M, N, K", [(1701, 1899, 145), (1793, 1793, 15), (1700, 1900, 1), (130, 14001, 300), (14001, 130, 1005),
+                                     (1281, 2561, 2005)])
+def test_any_sizes_in_large_tiles(M, N, K):
+    print("any, large", M, N, K, flush=True)
+    for out in TYPES:
+        run(M, N, K, out, bias=True)
