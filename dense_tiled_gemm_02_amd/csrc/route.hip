@@ -11,7 +11,13 @@
 // index, so that one integer maximum over the lanes gives both, and equal values
 // go to the lower index; a lane sorts its J keys by maxima and minima, and `top`
 // rounds of (maximum of the lanes' first keys, that lane moves its list up) give
-// the ids in order.  Bound by instructions, not by bytes.
+// the ids in order.  16 lanes where 16 logits each are enough: a round's maximum is
+// then four moves inside a quarter wave, and a wave has four rows under way.
+//
+// Bound by instructions, not by bytes: 16384 x 256 in bf16, top 8, 8.5 us (softmax),
+// 18 us (sigmoid with a bias), 20 us (and the best 4 of 8 groups by their best two);
+// its bytes take 2.  512 experts 12, 28 and 35 us, 64 experts 5 to 9.  The gradient
+// of 16384 x 256 7.3 us, of which its bytes are 3.5.
 //
 // Which of two experts comes first must not depend on rounding.  fp16 and bf16
 // logits without a bias are compared whole: the scores have the logits' order,
