@@ -107,7 +107,9 @@ const dtg::I8TileEntry* pick_tile(const gemm_i8_problem* p, const gemm_device_in
     // Rounds of workgroups times a tile's cost relative to 256 x 256, fitted to K =
     // 4096 (us a round): 256 x 256 53, 256 x 128 29.4, 128 x 256 31, 128 x 128 21.2, 64
     // x 64 12.7, and 19.4 with two to a CU.  A last round of at most half the CUs goes
-    // in halves (gemm_i8s_mixed_kernel).
+    // in halves (gemm_i8s_mixed_kernel).  192 x 256 is for what these leave between
+    // them (K = 4096, us of it, 256 x 256, the halves and 128 x 256: 1500 x 6000 42.5,
+    // 48.4, none, 57.6; 6000 x 6000 137, 167, 144, 153; 2500 x 8192 87.7, 102, 87.2, 91.8).
     const int64_t cus = dev->cu_count;
     auto cost = [&](const dtg::I8TileEntry& e) {
         const int64_t tiles = cdiv(p->M, e.bm) * cdiv(p->N, e.bn), left = tiles % cus;
@@ -116,7 +118,7 @@ const dtg::I8TileEntry* pick_tile(const gemm_i8_problem* p, const gemm_device_in
             const int64_t two = tiles % (2 * cus);
             return static_cast<double>(tiles / (2 * cus)) * 0.366 + (two == 0 ? 0.0 : two <= cus ? 0.24 : 0.366);
         }
-        return static_cast<double>(cdiv(tiles, cus)) * (e.bm + e.bn == 512 ? 1.0 : e.bm == 256 ? 0.56 : e.bn == 256 ? 0.59 : 0.4);
+        return static_cast<double>(cdiv(tiles, cus)) * (e.bm + e.bn == 512 ? 1.0 : e.bm == 192 ? 0.8 : e.bm == 256 ? 0.56 : e.bn == 256 ? 0.59 : 0.4);
     };
     int n = 0, best = -1;
     double best_t = 0.0;

@@ -56,6 +56,7 @@ hipError_t launch_mixed(const ScaledArgs& a, int64_t grid, hipStream_t stream) {
 const I8TileEntry kTable[] = {
     I8S_ALL(256, 256, 64, 2, 4, 16, 2),
     I8S_MIXED(kOutF16, "f16"), I8S_MIXED(kOutBF16, "bf16"), I8S_MIXED(kOutF32, "f32"),
+    I8S_ALL(192, 256, 64, 2, 4, 16, 2),
     I8S_ALL(256, 128, 64, 4, 2, 16, 3),
     I8S_ALL(128, 256, 64, 2, 4, 16, 3),
     I8S_ALL(128, 128, 64, 2, 4, 16, 4),

@@ -74,7 +74,7 @@ def test_every_kernel_runs():
             p = g.gemm_i8_problem()
             p.M, p.N, p.K, p.sx, p.sw, p.sy, p.out = M, N, 160, 160, 160, N, g.GEMM_BF16
             found.setdefault(i8.gemm_i8_plan_create(p).describe().split()[0], (M, N))
-    assert len(found) == 6 + 6   # of either table, one output type
+    assert len(found) == 7 + 6   # of either table, one output type
     for kernel, (M, N) in found.items():
         print(kernel, M, N, flush=True)
         run(M, N, 160, bias=True)
