@@ -322,21 +322,21 @@ struct NormFunction : torch::autograd::Function<NormFunction> {
 bool wants_grad(const at::Tensor& t) { return t.defined() && t.requires_grad(); }
 
 // A leaf's gradient is collected on the stream that its first live graph was
-// recorded on.  Where that is not the stream of a capture, the captured backward
-// pass would draw the other stream into the capture, and the process ends.
-void one_stream(const at::Tensor& leaf, const char* what) {
+// recorded on, which a captured backward pass draws into the capture.  The default
+// stream cannot be drawn in, and the process ends.
+void not_on_default_stream(const at::Tensor& leaf, const char* what) {
     if (!wants_grad(leaf) || !leaf.is_leaf()) return;
     const auto collector = torch::autograd::impl::try_get_grad_accumulator(leaf);
     if (!collector) return;
     const auto stream = collector->stream();
-    const c10::Stream now = c10::hip::getCurrentHIPStream(leaf.device().index()).unwrap();
-    if (stream && stream->id() != now.id())
-        throw std::runtime_error(std::string(what) + ": in a graph's capture, while a graph of the same leaf recorded on another "
-                                 "stream is alive; let go of that one first (its outputs, too), or record it on the capture's stream");
+    const c10::Stream bad = c10::hip::getDefaultHIPStream(leaf.device().index()).unwrap();
+    if (stream && stream->id() == bad.id())
+        throw std::runtime_error(std::string(what) + ": in a graph's capture, while a graph of the same leaf recorded on the default "
+                                 "stream is alive; let go of that one first (its outputs, too), or record it on another stream");
 }
 void capturable(const at::Tensor& a, const at::Tensor& b, const at::Tensor& c, const char* what) {
     if (c10::hip::currentStreamCaptureStatusMayInitCtx() == c10::hip::CaptureStatus::None) return;
-    for (const at::Tensor* t : {&a, &b, &c}) one_stream(*t, what);
+    for (const at::Tensor* t : {&a, &b, &c}) not_on_default_stream(*t, what);
 }
 
 // The outputs of an operator, in order.

@@ -52,7 +52,8 @@ def route(logits, top, score="softmax", bias=None, groups=1, top_groups=1, group
     bias).  Equal scores: the lowest index first.  An expert with a logit or bias
     of -inf or NaN is never chosen; ids that are left over are -1 with weight 0.
     The weights are differentiable (once) for the logits; in a graph's capture that
-    is refused while another stream's graph of the same leaf is alive.  Asynchronous
+    is refused while a graph of the same leaf that was recorded on the default
+    stream is alive.  Asynchronous
     on `stream` (default: torch's current stream)."""
     how = (top, SCORES.get(score, -1), groups, top_groups, group_best, 1 if renormalize else 0, float(scale))
     if stream is None:

@@ -156,7 +156,7 @@ def test_decoding_step_eager_and_captured(R):
 
 
 def test_capture_next_to_a_live_graph_of_the_same_leaves_is_refused():
-    """The captured backward pass would wait on the live graph's stream, which ends the process."""
+    """The captured backward pass would wait on the default stream, which ends the process."""
     x, logits = (torch.randn(8, 64, dtype=BF16, device="cuda", requires_grad=True) for _ in range(2))
     weight = torch.ones(64, device="cuda", requires_grad=True)
     alive = norm.rms_norm(x, weight), router.route(logits, 2)
@@ -176,7 +176,7 @@ def test_capture_next_to_a_live_graph_of_the_same_leaves_is_refused():
                 refusals.append(str(e))
         with torch.no_grad():   # no gradient, no collector
             norm.rms_norm(x, weight)
-    assert len(refusals) == len(calls) and all("another stream is alive" in r for r in refusals)
+    assert len(refusals) == len(calls) and all("default stream is alive" in r for r in refusals)
     graph.replay()
     torch.cuda.synchronize()
     assert out.tolist() == [1, 1, 1, 1]
@@ -227,3 +227,36 @@ def test_threads_with_streams_of_their_own():
     for seed, got in results.items():
         for a, b in zip(got, work(seed)):
             assert torch.equal(a, b)
+
+
+def test_capture_next_to_a_live_graph_of_another_stream():
+    """The usual warm-up: a graph of the same leaves, recorded on a side stream, is still referred to."""
+    x, logits = (torch.randn(8, 64, dtype=BF16, device="cuda", requires_grad=True) for _ in range(2))
+    weight = torch.ones(64, device="cuda", requires_grad=True)
+    dy, dw = torch.randn(8, 64, device="cuda").to(BF16), torch.randn(8, 2, device="cuda")
+
+    def step():
+        y, (w, _) = norm.rms_norm(x, weight), router.route(logits, 2)
+        return (y, w) + torch.autograd.grad((y, w), (x, weight, logits), (dy, dw))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        alive = step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for turn in range(3):
+        with torch.no_grad():
+            x += 1
+            logits *= 0.5
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.detach().clone() for t in captured]
+        with torch.cuda.stream(side):
+            want = step()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    assert alive[0].grad_fn is not None
