@@ -671,8 +671,9 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouteGradArgs a) {
 // Rows of a launch: of more, several follow one another.
 constexpr int64_t kMostRows = int64_t(1) << 24;
 
-// fn(lanes, logits a lane, kind) for E experts.
-template <typename Fn>
+// fn(lanes, logits a lane, kind) for E experts; GROUPED: there can be groups, which
+// want a lane each.
+template <bool GROUPED, typename Fn>
 hipError_t with_shape(int E, int groups, int kind, Fn&& fn) {
     const int L = E > 512 || groups > 32 ? 64 : E > 256 || groups > 16 ? 32 : 16;
     const int need = (E + L - 1) / L;
@@ -689,11 +690,13 @@ hipError_t with_shape(int E, int groups, int kind, Fn&& fn) {
     DTG_ROUTE(16, 4)
     DTG_ROUTE(16, 8)
     DTG_ROUTE(16, 16)
-    DTG_ROUTE(32, 1)
-    DTG_ROUTE(32, 4)
+    if constexpr (GROUPED) {
+        DTG_ROUTE(32, 1)
+        DTG_ROUTE(32, 4)
+        DTG_ROUTE(64, 1)
+        DTG_ROUTE(64, 4)
+    }
     DTG_ROUTE(32, 16)
-    DTG_ROUTE(64, 1)
-    DTG_ROUTE(64, 4)
     DTG_ROUTE(64, 16)
 #undef DTG_ROUTE
     return hipErrorInvalidValue;
@@ -704,7 +707,7 @@ unsigned grid_of(int64_t rows, int per) { return static_cast<unsigned>(((rows < 
 }  // namespace
 
 hipError_t launch_route(const RouteArgs& a, int kind, hipStream_t stream) {
-    return with_shape(a.E, a.groups, kind, [&](auto l, auto j, auto k) {
+    return with_shape<true>(a.E, a.groups, kind, [&](auto l, auto j, auto k) {
         constexpr int ROWS = kThreads / decltype(l)::value;
         // rows that are compared whole need no second choice, and no room for groups where they are lanes
         const bool spare = a.bias || a.groups > 1 || decltype(k)::value == 2;
@@ -728,7 +731,7 @@ hipError_t launch_route(const RouteArgs& a, int kind, hipStream_t stream) {
 }
 
 hipError_t launch_route_grad(const RouteGradArgs& a, int kind, hipStream_t stream) {
-    return with_shape(a.E, 1, kind, [&](auto l, auto j, auto k) {
+    return with_shape<false>(a.E, 1, kind, [&](auto l, auto j, auto k) {
         constexpr int ROWS = kThreads / decltype(l)::value;
         RouteGradArgs g = a;
         for (g.first = 0; g.first < a.R; g.first += kMostRows)
