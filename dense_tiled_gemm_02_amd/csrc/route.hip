@@ -84,11 +84,14 @@ __device__ __forceinline__ double row_sum(double v) {
     return v;
 }
 
-// e^v by the hardware's 2^t, with t's rounding made up for: three steps of 2^-24
-// off at most, whatever v is (the bare 2^t: |v| steps).  Past +-200 it is that.
+// e^v by the hardware's 2^t, with t's rounding made up for: for v up to 88 three
+// steps of 2^-24 off at most (the bare 2^t: |v| steps), and 0 where e^v is below
+// 2^-126.  Past 88 it stays at e^88: an infinite 2^t times a rest that is zero or
+// negative would be a NaN.  Only the scores of a sigmoid ask for such a v, and
+// their 1 / (1 + e^88) is zero to every key.
 __device__ __forceinline__ float quick_exp(float v) {
     constexpr float hi = 1.44269502f, lo = 1.92596299e-8f, ln2 = 0.693147181f;   // hi + lo = log2 e
-    v = fminf(fmaxf(v, -200.0f), 200.0f);
+    v = fminf(fmaxf(v, -200.0f), 88.0f);
     const float t = v * hi, rest = fmaf(v, lo, fmaf(v, hi, -t));
     const float e = __builtin_amdgcn_exp2f(t);
     return fmaf(e, rest * ln2, e);
