@@ -27,6 +27,7 @@
 // the launch, which waits while the GPU's queue is full.
 #include <Python.h>
 #include <ATen/ATen.h>
+#include <c10/core/AutogradState.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPStream.h>
@@ -252,6 +253,13 @@ variable_list once(variable_list grads, const char* what) {
     return (*error)(std::move(grads));
 }
 
+// There is no forward-mode derivative: whoever asks for one is told, whether or
+// not the tensor requires a gradient (a dual number need not).
+void no_tangent(const at::Tensor& t, const char* what) {
+    if (t.defined() && c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined())
+        throw std::runtime_error(std::string(what) + " has no forward-mode derivative");
+}
+
 gemm_norm_problem norm_problem(const at::Tensor& x, const at::Tensor& w, const at::Tensor& r, double eps, int64_t sy) {
     gemm_norm_problem p = {};
     p.R = x.size(0);
@@ -296,6 +304,7 @@ struct NormFunction : torch::autograd::Function<NormFunction> {
     static variable_list backward(AutogradContext* ctx, variable_list grads) {
         const auto saved = ctx->get_saved_variables();
         const at::Tensor &h = saved[0], &w = saved[1], &rstd = saved[2];
+        for (const at::Tensor& g : grads) no_tangent(g, "the gradient of rms_norm");
         const at::Tensor dy = as_rows(grads[0]), dh = grads.size() > 1 ? as_rows(grads[1]) : at::Tensor();
         const c10::DeviceGuard guard(h.device());
         at::Tensor dx = dh, dw;
@@ -341,6 +350,7 @@ void capturable(const at::Tensor& a, const at::Tensor& b, const at::Tensor& c, c
 
 // The outputs of an operator, in order.
 variable_list norm_call(const at::Tensor& x, const at::Tensor& w, const at::Tensor& r, double eps) {
+    for (const at::Tensor* t : {&x, &w, &r}) no_tangent(*t, "rms_norm");
     if (at::GradMode::is_enabled() && (wants_grad(x) || wants_grad(w) || wants_grad(r))) {
         capturable(x, w, r, "rms_norm");
         return NormFunction::apply(x, w, r.defined() ? std::optional<at::Tensor>(r) : std::nullopt, eps);
@@ -417,6 +427,7 @@ struct RouteFunction : torch::autograd::Function<RouteFunction> {
 
     static variable_list backward(AutogradContext* ctx, variable_list grads) {
         if (!grads[0].defined()) return {at::Tensor(), at::Tensor(), at::Tensor(), at::Tensor()};
+        no_tangent(grads[0], "the gradient of route");
         const auto saved = ctx->get_saved_variables();
         const at::Tensor &logits = saved[0], &ids = saved[1];
         const auto v = ctx->saved_data["v"].toIntVector();
@@ -434,6 +445,7 @@ struct RouteFunction : torch::autograd::Function<RouteFunction> {
 };
 
 variable_list route_call(const at::Tensor& logits, const at::Tensor& bias, const RouteParameters& a) {
+    no_tangent(logits, "route");
     if (at::GradMode::is_enabled() && wants_grad(logits)) {
         capturable(logits, at::Tensor(), at::Tensor(), "route");
         return RouteFunction::apply(logits, bias.defined() ? std::optional<at::Tensor>(bias) : std::nullopt,

@@ -110,9 +110,10 @@ def rms_norm(x, weight, residual=None, eps=1e-6, stream=None):
 
     x, residual: R x K, float16 or bfloat16, unit stride along the rows; weight: K
     values of that type or float32.  Sums in float32, y rounded once.
-    Differentiable (once); in a graph's capture that is refused while a graph of
-    the same leaf that was recorded on the default stream is alive.  Asynchronous on `stream` (default:
-    torch's current stream)."""
+    Differentiable (once, and in reverse mode: a forward-mode dual is refused); in a
+    graph's capture that is refused while a graph of the same leaf that was recorded
+    on the default stream is alive.  Asynchronous on `stream` (default: torch's
+    current stream)."""
     eps = float(eps)
     if stream is None:
         out = _remembered(NORM, eps, x, weight, residual)

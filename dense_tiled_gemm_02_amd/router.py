@@ -51,10 +51,10 @@ def route(logits, top, score="softmax", bias=None, groups=1, top_groups=1, group
     part (strength: the sum of a group's best group_best, 1 or 2, scores with
     bias).  Equal scores: the lowest index first.  An expert with a logit or bias
     of -inf or NaN is never chosen; ids that are left over are -1 with weight 0.
-    The weights are differentiable (once) for the logits; in a graph's capture that
-    is refused while a graph of the same leaf that was recorded on the default
-    stream is alive.  Asynchronous
-    on `stream` (default: torch's current stream)."""
+    The weights are differentiable for the logits (once, and in reverse mode:
+    forward-mode dual logits are refused); in a graph's capture that is refused while
+    a graph of the same leaf that was recorded on the default stream is alive.
+    Asynchronous on `stream` (default: torch's current stream)."""
     how = (top, SCORES.get(score, -1), groups, top_groups, group_best, 1 if renormalize else 0, float(scale))
     if stream is None:
         pair = _remembered(ROUTE, how, logits, bias)
