@@ -213,7 +213,7 @@ gemm_status gemm_rms_norm_grad(const gemm_norm_problem* prob, const void* dy, co
         if (st != GEMM_OK) return st;
     }
     if (!dw) return GEMM_OK;   // without rows: zeros
-    return launched(dtg::launch_norm_weight_grad(static_cast<const float*>(workspace),
+    return launched(dtg::launch_norm_weight_grad(static_cast<float*>(workspace),
                                                  p->R > 0 ? dtg::norm_grad_parts(p->R, p->K) : 0, p->K, dw,
                                                  p->weight == GEMM_F32 ? 2 : p->weight == GEMM_BF16 ? 1 : 0, on),
                     "norm's weight gradient");

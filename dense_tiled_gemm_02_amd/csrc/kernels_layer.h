@@ -45,6 +45,7 @@ hipError_t launch_rows(const RowsArgs& a, int bf16, hipStream_t stream);
 int64_t norm_grad_parts(int64_t R, int64_t K);
 hipError_t launch_norm_grad(const NormGradArgs& a, int bf16, hipStream_t stream);
 // dw[k] = sum of the parts' k, in order; dw is fp32 (kind 2), bf16 (1) or fp16 (0).
-hipError_t launch_norm_weight_grad(const float* parts, int64_t nparts, int64_t K, void* dw, int kind, hipStream_t stream);
+// The parts may be overwritten.
+hipError_t launch_norm_weight_grad(float* parts, int64_t nparts, int64_t K, void* dw, int kind, hipStream_t stream);
 
 }  // namespace dtg

@@ -458,9 +458,11 @@ gemm_status gemm_i8_quantize(const void* x, gemm_dtype dtype, int64_t R, int64_t
  *     dx = w dy / n - h (sum_k w dy h) / (K n^3) + dh        (x's, and r's)
  *     dw = sum over the rows of dy h / n                     (of w's type)
  * dh (with has_residual, required then): the gradient of h as an output.
- * Strides: sy of dy, sr of dh, sh of h, sx of dx.  dw may be NULL: not wanted,
- * and no workspace needed; else workspace is 16-byte aligned, with no
- * preparation, for one call at a time, overlapping nothing. */
+ * Strides: sy of dy, sr of dh, sh of h, sx of dx.  dw: fp32 sums of at most 380
+ * additions in a row, for any R (off by 2^-15 of the terms' magnitudes at the very
+ * most), rounded to w's type.  dw may be NULL: not wanted, and no workspace
+ * needed; else workspace is 16-byte aligned, with no preparation, for one call at
+ * a time, overlapping nothing. */
 gemm_status gemm_rms_norm_grad_workspace(const gemm_norm_problem* prob, size_t* bytes);
 gemm_status gemm_rms_norm_grad(const gemm_norm_problem* prob, const void* dy, const void* dh, const void* h,
                                const void* w, const float* rstd, void* dx, void* dw, void* workspace,
