@@ -24,6 +24,7 @@ struct RowsArgs {
     int64_t R, sx, sr, sh, sy;
     int32_t K, w32;
     float eps;
+    float by;              // filled in by launch_rows: 1, or what values are scaled by before they are squared
 };
 
 // dx = dh + (g - h c) rstd with g = dy w, c = rstd^2 mean(g h); parts: per

@@ -148,9 +148,15 @@ __device__ __forceinline__ void weights8(const void* w, int w32, int k, int K, f
     }
 }
 
-// A sum of squares that overflows (bf16 values past 1e19) is taken again, of the
-// values scaled by this.
-constexpr float kSmaller = 0x1p-100f;
+// bf16 values whose squares fp32 cannot hold.  Where the mean plus eps is infinite
+// (values past 1e19, or the largest eps), it is taken again, of values scaled by
+// kSmaller.  Where eps is below kLeastEps, squares below 2^-126 can count beside it
+// and have lost their last bits: such a launch scales all values by kLarger
+// (RowsArgs::by; powers of two change no other bit), and eps by its square, which is
+// then 2^-117 and more.  Values that overflow with that, 2^36 and more, are not lost
+// to kSmaller.  Rows held in registers are not scaled (16384 x 2048 into int8 44.4
+// us, 46.1 with the factor), so these launches take shapes that read rows again.
+constexpr float kSmaller = 0x1p-80f, kLarger = 0x1p16f, kLeastEps = 0x1p-100f;
 
 // Eight quotients v / s as bytes.  v times the reciprocal of s, added to 1.5 x 2^23,
 // leaves the nearest integer in the sum's low bits; it is the division's wherever
@@ -263,11 +269,12 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rows_kernel(RowsArgs a) {
                 });
                 return meet.sum(ss);
             };
-            const float ss = squares(false, 1.0f);
+            const float by = BF16 && C == 0 ? a.by : 1.0f;
+            const float mean = squares(false, by) / static_cast<float>(K) + a.eps;
             // rows of one wave meet by lanes alone; of several, every thread of the workgroup is here
-            if (BF16 && __builtin_expect(ss == kInf, 0))
+            if (BF16 && __builtin_expect(mean == kInf, 0))
                 rstd = kSmaller / sqrtf(squares(true, kSmaller) / static_cast<float>(K) + a.eps * kSmaller * kSmaller);
-            else rstd = 1.0f / sqrtf(ss / static_cast<float>(K) + a.eps);
+            else rstd = by / sqrtf(mean);
             if (a.rstd && live && t == 0) a.rstd[row] = rstd;
         }
         auto values = [&](int k, u32x4 u, float (&v)[8]) {
@@ -561,7 +568,8 @@ constexpr int64_t kMostGroups = int64_t(1) << 20;   // workgroups of a launch; e
 
 template <bool BF16, bool NORM, bool QUANT>
 hipError_t launch_rows_as(const RowsArgs& a, hipStream_t stream) {
-    return with_shape(shape_of(a.R, a.K), [&](auto t_tag, auto c_tag) {
+    const Shape again = {a.K <= 512 ? 16 : 1024, 0};
+    return with_shape(a.by != 1.0f ? again : shape_of(a.R, a.K), [&](auto t_tag, auto c_tag) {
         constexpr int T = decltype(t_tag)::value, C = decltype(c_tag)::value;
         constexpr int THREADS = T < 256 ? 256 : T, ROWS = THREADS / T;
         const int64_t need = (a.R + ROWS - 1) / ROWS;
@@ -573,7 +581,13 @@ hipError_t launch_rows_as(const RowsArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_rows(const RowsArgs& a, int bf16, hipStream_t stream) {
+hipError_t launch_rows(const RowsArgs& given, int bf16, hipStream_t stream) {
+    RowsArgs a = given;
+    a.by = 1.0f;
+    if (a.w && bf16 && a.eps < kLeastEps) {
+        a.by = kLarger;
+        a.eps *= kLarger * kLarger;
+    }
     if (!a.w) return bf16 ? launch_rows_as<true, false, true>(a, stream) : launch_rows_as<false, false, true>(a, stream);
     if (a.q) return bf16 ? launch_rows_as<true, true, true>(a, stream) : launch_rows_as<false, true, true>(a, stream);
     return bf16 ? launch_rows_as<true, true, false>(a, stream) : launch_rows_as<false, true, false>(a, stream);
