@@ -31,6 +31,7 @@
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -148,6 +149,25 @@ struct Unlocked {   // the interpreter's lock, released
     PyThreadState* state = PyEval_SaveThread();
     ~Unlocked() { PyEval_RestoreThread(state); }
 };
+
+// The exception in flight as torch raises it: an allocation's by its own type, one
+// that a Python hook raised as it is.
+PyObject* raised() {
+    try {
+        throw;
+    } catch (python_error& ex) {
+        if (!PyErr_Occurred()) ex.restore();
+    } catch (const c10::OutOfMemoryError& ex) {
+        PyObject* const torch = PyImport_ImportModule("torch");
+        PyObject* const type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+        if (type) PyErr_SetString(type, ex.what_without_backtrace());
+        Py_XDECREF(type);
+        Py_XDECREF(torch);
+    } catch (const std::exception& ex) {
+        PyErr_SetString(PyExc_RuntimeError, ex.what());
+    }
+    return nullptr;
+}
 
 struct Held {   // a reference
     PyObject* o;
@@ -511,9 +531,8 @@ PyObject* py_row_operator(PyObject*, PyObject* const* args, Py_ssize_t n) {
     }
     try {
         return row_operator(KIND, n > tensors ? args[tensors] : Py_None, args);
-    } catch (const std::exception& ex) {
-        PyErr_SetString(PyExc_RuntimeError, ex.what());
-        return nullptr;
+    } catch (const std::exception&) {
+        return raised();
     }
 }
 
@@ -570,9 +589,8 @@ PyObject* py_call(PyObject*, PyObject* const* args, Py_ssize_t n) {
         PyTuple_SET_ITEM(pair, 0, THPVariable_Wrap(std::move(r.out)));
         PyTuple_SET_ITEM(pair, 1, THPVariable_Wrap(std::move(r.order)));
         return pair;
-    } catch (const std::exception& ex) {
-        PyErr_SetString(PyExc_RuntimeError, ex.what());
-        return nullptr;
+    } catch (const std::exception&) {
+        return raised();
     }
 }
 
@@ -608,9 +626,8 @@ PyObject* py_remember(PyObject*, PyObject* args) {
         if (calls.size() >= kMostCalls) forget(kind);   // ragged row counts: one entry each
         e.owner = owner;
         if (calls.emplace(key, std::move(e)).second) Py_INCREF(owner);
-    } catch (const std::exception& ex) {
-        PyErr_SetString(PyExc_RuntimeError, ex.what());
-        return nullptr;
+    } catch (const std::exception&) {
+        return raised();
     }
     Py_RETURN_NONE;
 }
