@@ -186,6 +186,13 @@ def _on_stream(fn, device, stream, inputs):
             return fn()
 
 
+def _written(out):
+    """The caller's `out`, noted as modified: autograd then finds a value that it
+    holds for a backward pass overwritten."""
+    torch.autograd.graph.increment_version(out)
+    return out
+
+
 def _offsets_arg(offsets, groups, device):
     if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] != groups + 1:
         raise ValueError("offsets must be %d int32 values, got %s %s" % (groups + 1, offsets.dtype,
@@ -263,7 +270,7 @@ def grouped_matmul(A, B, offsets, out=None, config=None, stream=None):
         raise ValueError("out must be %s of %dx%d" % (A.dtype, R, N))
 
     def call():
-        D = out if out is not None else torch.empty((R, N), dtype=A.dtype, device=A.device)
+        D = _written(out) if out is not None else torch.empty((R, N), dtype=A.dtype, device=A.device)
         plan = _run(GEMM_GROUPED_ROWS, A, B, offsets, D, E, K, N, False, config)
         if plain:
             _remember(MATMUL, plan, "gemm_grouped_run_parts", plan.workspace, (R, N), A.dtype, None, A, B, offsets)
@@ -299,7 +306,7 @@ def grouped_wgrad(A, G, offsets, out=None, out_dtype=None, accumulate=False, con
         raise ValueError("out must be %dx%dx%d" % (E, K, N))
 
     def call():
-        D = out if out is not None else torch.empty((E, K, N), dtype=dtype, device=A.device)
+        D = _written(out) if out is not None else torch.empty((E, K, N), dtype=dtype, device=A.device)
         plan = _run(GEMM_GROUPED_REDUCE, A, G, offsets, D, E, K, N, accumulate, config)
         if plain:
             _remember(WGRAD, plan, "gemm_grouped_run_parts", plan.workspace, (E, K, N), dtype, out_dtype, A, G, offsets)

@@ -13,7 +13,7 @@ import threading
 import torch
 
 from . import GEMM_BF16, GEMM_F16, GEMM_F32, _check, _keep_plan, _p, gemm_i8_problem, lib
-from .grouped import I8, I8_ROWS, _need_gpu, _on_stream, _raw_stream, _remember, _remembered, _row_operator
+from .grouped import I8, I8_ROWS, _need_gpu, _on_stream, _raw_stream, _remember, _remembered, _row_operator, _written
 from .norm import _rows_arg
 
 _CODES = {torch.float16: GEMM_F16, torch.bfloat16: GEMM_BF16, torch.float32: GEMM_F32}
@@ -122,7 +122,7 @@ def i8_matmul(X, x_scale, W, w_scale, bias=None, out_dtype=torch.bfloat16, out=N
     _need_gpu(X.device, ("X", X), ("W", W), ("x_scale", x_scale), ("w_scale", w_scale), ("bias", bias), ("out", out))
 
     def call():
-        Y = out if out is not None else torch.empty((M, N), dtype=dtype, device=X.device)
+        Y = _written(out) if out is not None else torch.empty((M, N), dtype=dtype, device=X.device)
         key = (X.device.index, dtype, M, N, K, X.stride(0), W.stride(0), Y.stride(0), bias is None)
         plan = _plans.get(key)
         if plan is None:

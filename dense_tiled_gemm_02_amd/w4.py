@@ -12,7 +12,7 @@ import threading
 import torch
 
 from . import GEMM_BF16, GEMM_F16, _check, _keep_plan, _p, gemm_w4_problem, lib
-from .grouped import W4, _need_gpu, _on_stream, _raw_stream, _remember, _remembered
+from .grouped import W4, _need_gpu, _on_stream, _raw_stream, _remember, _remembered, _written
 
 _CODES = {torch.float16: GEMM_F16, torch.bfloat16: GEMM_BF16}
 
@@ -103,7 +103,7 @@ def w4_matvec(X, W, scale, zeros=None, group=128, experts=None, out=None, stream
     _need_gpu(X.device, ("X", X), ("W", W), ("scale", scale), ("zeros", zeros), ("experts", experts), ("out", out))
 
     def call():
-        Y = out if out is not None else torch.empty((M, N), dtype=X.dtype, device=X.device)
+        Y = _written(out) if out is not None else torch.empty((M, N), dtype=X.dtype, device=X.device)
         if experts is not None and W.shape[0] == 0:   # no matrix: every row is outside
             return Y.zero_()
         key = (X.device.index, X.dtype, M, X.stride(0), W.shape, W.stride(), scale.stride(),
