@@ -50,7 +50,8 @@ def route(logits, top, score="softmax", bias=None, groups=1, top_groups=1, group
     groups: the experts in that many runs, of which the top_groups strongest take
     part (strength: the sum of a group's best group_best, 1 or 2, scores with
     bias).  Equal scores: the lowest index first.  An expert with a logit or bias
-    of -inf or NaN is never chosen; ids that are left over are -1 with weight 0.
+    of -inf or NaN is never chosen; ids that are left over are -1 with weight 0.  A
+    row with a NaN logit has NaN weights, and the gradient of the row with -inf there.
     The weights are differentiable for the logits (once, and in reverse mode:
     forward-mode dual logits are refused); in a graph's capture that is refused while
     a graph of the same leaf that was recorded on the default stream is alive.

@@ -510,12 +510,13 @@ gemm_status gemm_i8_run(const gemm_i8_plan* plan, const int8_t* X, const float* 
  *    renormalize.  The bias moves the choice alone.
  * What is compared is exact: the logits themselves without a bias (the scores
  * have their order), else scores in 64 bits wherever fp32 could confuse two.
- * Weights are computed and written in fp32.
+ * Weights are computed and written in fp32; a share below 2^-126 is 0.
  *
  * An expert whose logit or bias is -infinity or NaN is never chosen (and adds
  * nothing to a group's strength); where fewer than `top` are left, the last ids
  * are -1 with the weight 0, which gemm_group_rows and gemm_w4_run take as no
- * group.  A row with a NaN logit has NaN for the weights of its chosen experts.
+ * group.  A row with a NaN logit has NaN for the weights of its chosen experts;
+ * its gradient is the one of the same row with -infinity in place of the NaNs.
  *
  * gemm_route_grad: dlogits (R x E, the logits' type) from dweights (R x top),
  * the ids that were chosen, and the logits.  The choice has no gradient, nor
