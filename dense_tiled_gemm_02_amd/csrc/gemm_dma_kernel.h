@@ -228,7 +228,8 @@ __device__ __forceinline__ void dma_tile_in(uint16_t* const smem, const KArgs& p
     const uint32_t smem0 = lds_addr(smem);
 
     // The tile's scales go to LDS ahead of the ring's loads (whose waits are
-    // then for them, too): 64 floats of A's rows or B's columns to a load, zeros
+    // then for them, too: such a tile has a K step, products over no k run
+    // i8_any_kernel): 64 floats of A's rows or B's columns to a load, zeros
     // past the last.
     __shared__ __attribute__((aligned(16))) float row_col[SCALED ? BM + BN : 4];
     if constexpr (SCALED) {
@@ -551,8 +552,6 @@ __device__ __forceinline__ void dma_tile_in(uint16_t* const smem, const KArgs& p
         }
         // no load may still be writing this workgroup's LDS when it exits
         wait_vm<0>();
-    } else if constexpr (SCALED) {
-        wait_vm<0>();   // the scales' loads
     }
     if constexpr (AGPR) agpr_settle();
 
