@@ -1,14 +1,13 @@
 // C ABI of the int8 products with scales: validation, variant choice and
 // launch.  Declarations and the contract are in include/gemm.h.
 #include <hip/hip_runtime.h>
-#include <stdarg.h>
 #include <stdint.h>
 #include <stdio.h>
 
 #include <new>
 
 #include "../../include/gemm.h"
-#include "api_internal.h"
+#include "api_operands.h"
 #include "kernels_i8.h"
 
 struct gemm_i8_plan {
@@ -22,27 +21,14 @@ struct gemm_i8_plan {
 
 namespace {
 
-gemm_status fail(gemm_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-gemm_status fail(gemm_status st, const char* fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    return dtg::record_error(st, buf);
-}
+using dtg::extent;
+using dtg::fail;
+using dtg::Operand;
 
 constexpr int64_t kMaxRows = int64_t(1) << 27;        // of X and W: the grids of the smallest tiles
 constexpr int64_t kMaxOutputs = int64_t(1) << 35;
 constexpr int64_t kMaxK = int64_t(1) << 17;           // 2^17 products of 2^14 make 2^31
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// Bytes from the first to one past the last of `rows` rows of `cols`, or -1 past 2^60.
-int64_t extent(int64_t rows, int64_t stride, int64_t cols, int64_t size) {
-    if (rows <= 0 || cols <= 0) return 0;
-    const __int128 e = (static_cast<__int128>(rows - 1) * stride + cols) * size;
-    return e > (static_cast<__int128>(1) << 60) ? -1 : static_cast<int64_t>(e);
-}
 
 int out_bytes(const gemm_i8_problem* p) { return p->out == GEMM_F32 ? 4 : 2; }
 
@@ -164,13 +150,6 @@ gemm_status plan_impl(const gemm_i8_problem* given, const gemm_device_info* dev,
     return GEMM_OK;
 }
 
-struct Operand {
-    const char* name;
-    const void* p;
-    int64_t bytes;
-    int align;
-};
-
 }  // namespace
 
 extern "C" {
@@ -205,21 +184,14 @@ gemm_status gemm_i8_run(const gemm_i8_plan* plan, const int8_t* X, const float* 
     if (!p.has_bias && bias) return fail(GEMM_ERR_INVALID_ARG, "bias given but the problem has has_bias = 0");
     if (p.M == 0 || p.N == 0) return GEMM_OK;
     const int size = out_bytes(&p);
-    const Operand y = {"Y", Y, extent(p.M, p.sy, p.N, size), size};
-    const Operand in[5] = {{"X", X, extent(p.M, p.sx, p.K, 1), 1},
-                           {"W", W, extent(p.N, p.sw, p.K, 1), 1},
-                           {"x_scale", x_scale, p.M * 4, 4},
-                           {"w_scale", w_scale, p.N * 4, 4},
-                           {"bias", bias, p.has_bias ? p.N * size : 0, size}};
-    if (!Y) return fail(GEMM_ERR_INVALID_ARG, "Y is NULL");
-    if (reinterpret_cast<uintptr_t>(Y) % size) return fail(GEMM_ERR_UNSUPPORTED, "Y must be aligned to its element size");
-    for (const Operand& o : in) {
-        if (o.bytes == 0) continue;
-        if (!o.p) return fail(GEMM_ERR_INVALID_ARG, "%s is NULL", o.name);
-        const uintptr_t a = reinterpret_cast<uintptr_t>(o.p), b = reinterpret_cast<uintptr_t>(y.p);
-        if (a % o.align) return fail(GEMM_ERR_UNSUPPORTED, "%s must be aligned to its element size", o.name);
-        if (a < b + y.bytes && b < a + o.bytes) return fail(GEMM_ERR_INVALID_ARG, "Y overlaps %s", o.name);
-    }
+    const Operand o[6] = {{"X", X, extent(p.M, p.sx, p.K, 1), 1, false},
+                          {"W", W, extent(p.N, p.sw, p.K, 1), 1, false},
+                          {"x_scale", x_scale, p.M * 4, 4, false},
+                          {"w_scale", w_scale, p.N * 4, 4, false},
+                          {"bias", bias, p.has_bias ? p.N * size : 0, size, false},
+                          {"Y", Y, extent(p.M, p.sy, p.N, size), size, true}};
+    const gemm_status st = dtg::check(o, 6);
+    if (st != GEMM_OK) return st;
     const dtg::ScaledI8 scales = {x_scale, w_scale, p.has_bias ? bias : nullptr};
     const hipStream_t on = static_cast<hipStream_t>(stream);
     const bool aligned = reinterpret_cast<uintptr_t>(X) % 16 == 0 && reinterpret_cast<uintptr_t>(W) % 16 == 0;
@@ -258,7 +230,7 @@ gemm_status gemm_i8_run(const gemm_i8_plan* plan, const int8_t* X, const float* 
         a.ly = p.sy;
         err = plan->few && aligned ? plan->few->launch[plan->out](a, on) : dtg::launch_i8_any(a, plan->out, plan->cus, plan->xcds, on);
     }
-    return err == hipSuccess ? GEMM_OK : fail(GEMM_ERR_HIP, "launch of the int8 product: %s", hipGetErrorString(err));
+    return dtg::launched(err, "int8 product");
 }
 
 }  // extern "C"

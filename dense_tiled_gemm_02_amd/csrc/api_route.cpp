@@ -2,25 +2,19 @@
 // Declarations and the contract are in include/gemm.h.
 #include <hip/hip_runtime.h>
 #include <math.h>
-#include <stdarg.h>
 #include <stdint.h>
 #include <stdio.h>
 
 #include "../../include/gemm.h"
-#include "api_internal.h"
+#include "api_operands.h"
 #include "kernels_route.h"
 
 namespace {
 
-gemm_status fail(gemm_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-gemm_status fail(gemm_status st, const char* fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    return dtg::record_error(st, buf);
-}
+using dtg::check;
+using dtg::fail;
+using dtg::launched;
+using dtg::Operand;
 
 gemm_status validate(const gemm_route_problem* p) {
     if (!p) return fail(GEMM_ERR_INVALID_ARG, "problem is NULL");
@@ -52,39 +46,9 @@ gemm_status validate(const gemm_route_problem* p) {
     return GEMM_OK;
 }
 
-struct Operand {
-    const char* name;
-    const void* p;
-    int64_t bytes;
-    int align;
-    bool written;
-};
-
-// Addresses there and aligned, no output overlapping anything.
-gemm_status check(const Operand* o, int n) {
-    for (int i = 0; i < n; ++i) {
-        if (o[i].bytes == 0) continue;
-        if (!o[i].p) return fail(GEMM_ERR_INVALID_ARG, "%s is NULL", o[i].name);
-        if (reinterpret_cast<uintptr_t>(o[i].p) % o[i].align)
-            return fail(GEMM_ERR_UNSUPPORTED, "%s must be aligned to its element size", o[i].name);
-    }
-    for (int i = 0; i < n; ++i)
-        for (int j = 0; j < n; ++j) {
-            if (i == j || !o[i].written || o[i].bytes == 0 || o[j].bytes == 0) continue;
-            const uintptr_t a = reinterpret_cast<uintptr_t>(o[i].p), b = reinterpret_cast<uintptr_t>(o[j].p);
-            if (a < b + o[j].bytes && b < a + o[i].bytes)
-                return fail(GEMM_ERR_INVALID_ARG, "%s overlaps %s", o[i].name, o[j].name);
-        }
-    return GEMM_OK;
-}
-
 int64_t size_of(const gemm_route_problem* p) { return p->dtype == GEMM_F32 ? 4 : 2; }
 int64_t logit_bytes(const gemm_route_problem* p) { return p->R > 0 ? ((p->R - 1) * p->sl + p->E) * size_of(p) : 0; }
 int kind_of(const gemm_route_problem* p) { return p->dtype == GEMM_F32 ? 2 : p->dtype == GEMM_BF16 ? 1 : 0; }
-
-gemm_status launched(hipError_t err, const char* what) {
-    return err == hipSuccess ? GEMM_OK : fail(GEMM_ERR_HIP, "launch of the %s: %s", what, hipGetErrorString(err));
-}
 
 }  // namespace
 
