@@ -39,6 +39,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <initializer_list>
 #include <unordered_map>
 #include <utility>
 
@@ -263,6 +264,16 @@ at::Tensor as_rows(const at::Tensor& t) {
     return !t.defined() || t.size(1) <= 1 || t.stride(1) == 1 ? t : t.contiguous();
 }
 
+// A saved tensor as it was: hooks may give back another layout, which is taken, and
+// anything else, which must not reach a kernel.
+at::Tensor as_saved(const at::Tensor& t, const at::Tensor& like, at::IntArrayRef sizes, std::initializer_list<at::ScalarType> types) {
+    if (!t.defined() || t.layout() != at::kStrided || t.device() != like.device() || t.sizes() != sizes ||
+        std::find(types.begin(), types.end(), t.scalar_type()) == types.end())
+        throw std::runtime_error("a saved tensor came back from a hook on another device, of another type or of another shape");
+    const at::Tensor r = t.resolve_neg();
+    return r.size(-1) <= 1 || r.stride(-1) == 1 ? r : r.contiguous();
+}
+
 // These gradients have none of their own: whoever differentiates them is told.
 variable_list once(variable_list grads, const char* what) {
     if (!at::GradMode::is_enabled()) return grads;
@@ -323,12 +334,14 @@ struct NormFunction : torch::autograd::Function<NormFunction> {
 
     static variable_list backward(AutogradContext* ctx, variable_list grads) {
         const auto saved = ctx->get_saved_variables();
-        const at::Tensor &h = saved[0], &w = saved[1], &rstd = saved[2];
         for (const at::Tensor& g : grads) no_tangent(g, "the gradient of rms_norm");
         const at::Tensor dy = as_rows(grads[0]), dh = grads.size() > 1 ? as_rows(grads[1]) : at::Tensor();
-        const c10::DeviceGuard guard(h.device());
         at::Tensor dx = dh, dw;
         if (dy.defined()) {
+            const at::Tensor h = as_saved(saved[0], dy, dy.sizes(), {dy.scalar_type()});
+            const at::Tensor w = as_saved(saved[1], dy, {dy.size(1)}, {dy.scalar_type(), at::kFloat});
+            const at::Tensor rstd = as_saved(saved[2], dy, {dy.size(0)}, {at::kFloat});
+            const c10::DeviceGuard guard(h.device());
             dx = make({h.size(0), h.size(1)}, h.scalar_type(), h);
             gemm_norm_problem p = norm_problem(dx, w, dh, 1.0, dy.stride(0));
             p.sh = h.stride(0);
@@ -449,13 +462,15 @@ struct RouteFunction : torch::autograd::Function<RouteFunction> {
         if (!grads[0].defined()) return {at::Tensor(), at::Tensor(), at::Tensor(), at::Tensor()};
         no_tangent(grads[0], "the gradient of route");
         const auto saved = ctx->get_saved_variables();
-        const at::Tensor &logits = saved[0], &ids = saved[1];
+        const at::Tensor dw = grads[0].contiguous().resolve_neg();
+        const int64_t experts = saved[0].defined() && saved[0].dim() == 2 ? saved[0].size(1) : 0;
+        const at::Tensor logits = as_saved(saved[0], dw, {dw.size(0), experts}, {at::kHalf, at::kBFloat16, at::kFloat});
+        const at::Tensor ids = as_saved(saved[1], dw, dw.sizes(), {at::kInt}).contiguous();
         const auto v = ctx->saved_data["v"].toIntVector();
         RouteParameters a;
         std::copy(v.begin(), v.end(), a.v);
         a.scale = ctx->saved_data["scale"].toDouble();
         const c10::DeviceGuard guard(logits.device());
-        const at::Tensor dw = grads[0].contiguous();
         at::Tensor dl = make({logits.size(0), logits.size(1)}, logits.scalar_type(), logits);
         const gemm_route_problem p = route_problem(logits, false, a);
         check_backward(library.route_grad(&p, data(logits), static_cast<const int32_t*>(data(ids)), static_cast<const float*>(data(dw)),
