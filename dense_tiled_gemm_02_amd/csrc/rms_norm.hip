@@ -579,6 +579,36 @@ hipError_t launch_rows_as(const RowsArgs& a, hipStream_t stream) {
     });
 }
 
+// Workgroups of the gradient over R rows of K, in one launch.  Each has a part, K floats
+// written and read again, so a workgroup takes four rows and more, down to one
+// workgroup to a CU; up to as many as keep the memory busy (1024 x 4096: 256 parts
+// 15.5 us, 512 17.1; 8192 x 4096: 52.6 with 512, 1024 63.6; 16384 x 1024: 768 30.2,
+// 1024 31.6).
+int64_t grad_rows(Shape s) { return s.t < 256 ? 256 / s.t : 1; }
+int64_t most_groups(Shape s) { return s.t >= 1024 ? 256 : s.t == 512 ? 512 : s.t == 64 ? 768 : 1024; }
+int64_t grad_groups(Shape s, int64_t R) {
+    const int64_t need = (R + grad_rows(s) - 1) / grad_rows(s);
+    int64_t n = (need + 3) / 4;
+    if (n < 256) n = 256;
+    if (n > most_groups(s)) n = most_groups(s);
+    return need < n ? need : n;
+}
+
+// Rows of a launch: in a longer one a thread's running fp32 sum for dw would take more
+// than 128 rows and lose the last bits of its terms.  An element of dw goes through at
+// most 128 + 15 additions in a row here, and 64 + 15 in each pass over the parts (one up
+// to 1024 parts, three at 2^31 rows).  (More workgroups in one launch take longer:
+// 262144 x 4096 1857 us in one of 2048, 1585 in four of 512, 1608 in one of 512.)
+int64_t grad_launch(Shape s) { return 128 * grad_rows(s) * most_groups(s); }
+
+template <bool FAR>
+void launch_sum(const float* parts, int n, int K, int64_t stride, void* dw, int kind, unsigned groups, hipStream_t stream) {
+    const dim3 grid(static_cast<unsigned>((K + 63) / 64), groups), block(64 * kSumWaves);
+    if (kind == 2) hipLaunchKernelGGL((norm_weight_grad_kernel<2, FAR>), grid, block, 0, stream, parts, n, K, stride, dw);
+    else if (kind == 1) hipLaunchKernelGGL((norm_weight_grad_kernel<1, FAR>), grid, block, 0, stream, parts, n, K, stride, dw);
+    else hipLaunchKernelGGL((norm_weight_grad_kernel<0, FAR>), grid, block, 0, stream, parts, n, K, stride, dw);
+}
+
 }  // namespace
 
 hipError_t launch_rows(const RowsArgs& given, int bf16, hipStream_t stream) {
@@ -593,46 +623,32 @@ hipError_t launch_rows(const RowsArgs& given, int bf16, hipStream_t stream) {
     return bf16 ? launch_rows_as<true, true, false>(a, stream) : launch_rows_as<false, true, false>(a, stream);
 }
 
-constexpr int64_t kRunRows = 128;
-
 int64_t norm_grad_parts(int64_t R, int64_t K) {
     const Shape s = grad_shape_of(K);
-    const int64_t rows = s.t < 256 ? 256 / s.t : 1, need = (R + rows - 1) / rows;
-    // Each part is K floats written and read again, so a workgroup takes four rows
-    // and more, down to one workgroup to a CU; up to as many as keep the memory busy
-    // (1024 x 4096: 256 parts 15.5 us, 512 17.1; 8192 x 4096: 52.6 with 512, 1024 63.6;
-    // 16384 x 1024: 768 30.2, 1024 31.6).
-    const int64_t most = s.t >= 1024 ? 256 : s.t == 512 ? 512 : s.t == 64 ? 768 : 1024;
-    int64_t n = (need + 3) / 4;
-    if (n < 256) n = 256;
-    if (n > most) n = most;
-    // A thread's running fp32 sum takes at most kRunRows rows, however many there are:
-    // the last bits of the terms would be lost in a longer one.  An element of dw then
-    // goes through at most 128 + 15 additions in a row here, and 64 + 15 in each pass over
-    // the parts (one up to 1024 parts, three at 2^31 rows).  Against parts without bound:
-    // 131072 x 8192 1307 us and 1233 (runs of 64: 1342), 262144 x 4096 975 and 1105 (964),
-    // 4194304 x 256 1788 and 2572 (1704).
-    const int64_t least = (need + kRunRows - 1) / kRunRows;
-    if (n < least) n = least;
-    return need < n ? need : n;
+    const int64_t rows = grad_launch(s);
+    return R / rows * grad_groups(s, rows) + grad_groups(s, R % rows);
 }
 
-hipError_t launch_norm_grad(const NormGradArgs& a, int bf16, hipStream_t stream) {
-    return with_grad_shape(grad_shape_of(a.K), [&](auto t_tag, auto c_tag) {
+hipError_t launch_norm_grad(const NormGradArgs& given, int bf16, hipStream_t stream) {
+    const Shape s = grad_shape_of(given.K);
+    return with_grad_shape(s, [&](auto t_tag, auto c_tag) {
         constexpr int T = decltype(t_tag)::value, C = decltype(c_tag)::value;
-        const dim3 grid(static_cast<unsigned>(norm_grad_parts(a.R, a.K))), block(T < 256 ? 256 : T);
-        if (bf16) hipLaunchKernelGGL((norm_grad_kernel<true, T, C>), grid, block, 0, stream, a);
-        else hipLaunchKernelGGL((norm_grad_kernel<false, T, C>), grid, block, 0, stream, a);
+        NormGradArgs a = given;
+        for (int64_t left = given.R; left > 0; left -= a.R) {
+            a.R = left < grad_launch(s) ? left : grad_launch(s);
+            const int64_t groups = grad_groups(s, a.R);
+            const dim3 grid(static_cast<unsigned>(groups)), block(T < 256 ? 256 : T);
+            if (bf16) hipLaunchKernelGGL((norm_grad_kernel<true, T, C>), grid, block, 0, stream, a);
+            else hipLaunchKernelGGL((norm_grad_kernel<false, T, C>), grid, block, 0, stream, a);
+            a.dy += a.R * a.sy;
+            a.h += a.R * a.sh;
+            if (a.dh) a.dh += a.R * a.sr;
+            a.dx += a.R * a.sx;
+            a.rstd += a.R;
+            if (a.parts) a.parts += groups * a.K;
+        }
         return hipGetLastError();
     });
-}
-
-template <bool FAR>
-void launch_sum(const float* parts, int n, int K, int64_t stride, void* dw, int kind, unsigned groups, hipStream_t stream) {
-    const dim3 grid(static_cast<unsigned>((K + 63) / 64), groups), block(64 * kSumWaves);
-    if (kind == 2) hipLaunchKernelGGL((norm_weight_grad_kernel<2, FAR>), grid, block, 0, stream, parts, n, K, stride, dw);
-    else if (kind == 1) hipLaunchKernelGGL((norm_weight_grad_kernel<1, FAR>), grid, block, 0, stream, parts, n, K, stride, dw);
-    else hipLaunchKernelGGL((norm_weight_grad_kernel<0, FAR>), grid, block, 0, stream, parts, n, K, stride, dw);
 }
 
 hipError_t launch_norm_weight_grad(float* parts, int64_t nparts, int64_t K, void* dw, int kind, hipStream_t stream) {
