@@ -67,12 +67,12 @@ bool near(int64_t rows, int64_t stride, int64_t K) {
 // The smallest tile of at most 64 x 32 whose workgroups the CUs hold at once: K is
 // long beside the tile, and its waves share it out, so that a second round or a
 // larger tile costs more than reading X or W again (us, W from memory):
-//   64 x 1024 x 1024   16 x 16 tiles 3.4, 32 x 32 4.1, 64 x 64 5.3
-//   32 x 4096 x 4096   16 x 32 7.3, 32 x 32 8.0; 16 x 16, two rounds 11
-//   128 x 4096 x 4096  64 x 32 10.2, 32 x 32, two rounds 12.3, 64 x 64 12.1
-//   64 x 14336 x 4096  64 x 64 16.3, 64 x 32, two rounds 20.7
+//   64 x 1024 x 1024   16 x 16 tiles 3.4, 32 x 32 4.1, 64 x 64 5.2
+//   32 x 4096 x 4096   16 x 32 7.1, 32 x 32 8.0; 16 x 16, two rounds 10.6
+//   128 x 4096 x 4096  64 x 32 10.2, 32 x 32, two rounds 12.4, 64 x 64 12.8
+//   64 x 14336 x 4096  64 x 64 16.2, 64 x 32, two rounds 20.7
 // Up to 32 rows the widest tile stays on where no tile fits: 32 x 28672 x 8192 42.9
-// us, 64 x 64 46.5.
+// us, 64 x 64 46.3.
 const dtg::I8FewEntry* pick_few(const gemm_i8_problem* p, const gemm_device_info* dev) {
     static const struct { int mb, nb, rows; } order[] = {{1, 1, 0}, {1, 2, 0}, {1, 4, 16}, {2, 2, 0}, {2, 4, 32}, {4, 2, 0}};
     int n = 0;
@@ -94,8 +94,10 @@ const dtg::I8TileEntry* pick_tile(const gemm_i8_problem* p, const gemm_device_in
     // 4096 (us a round): 256 x 256 53, 256 x 128 29.4, 128 x 256 31, 128 x 128 21.2, 64
     // x 64 12.7, and 19.4 with two to a CU.  A last round of at most half the CUs goes
     // in halves (gemm_i8s_mixed_kernel).  192 x 256 is for what these leave between
-    // them (K = 4096, us of it, 256 x 256, the halves and 128 x 256: 1500 x 6000 42.5,
-    // 48.4, none, 57.6; 6000 x 6000 137, 167, 144, 153; 2500 x 8192 87.7, 102, 87.2, 91.8).
+    // them (K = 4096, us of it, 256 x 256, the halves and 128 x 256: 1500 x 6000 48.9,
+    // 54.0, none, 58.3; 6000 x 6000 150, 160, 147, 158; 2500 x 8192 95.4, 113, 88.4, 92.9).
+    // Short K keeps the order: K = 512, 1500 x 6000 13.6, 14.8, none, 17.9; 6000 x 6000
+    // 42.5, 47.7, 43.1, 46.2; 4096 x 4096 23.4, 16.9, none, 20.3.
     const int64_t cus = dev->cu_count;
     auto cost = [&](const dtg::I8TileEntry& e) {
         const int64_t tiles = cdiv(p->M, e.bm) * cdiv(p->N, e.bn), left = tiles % cus;

@@ -10,10 +10,10 @@
 // The sums are exact (int32), so nothing depends on their order.
 //
 // Bound by the loads of single bytes' alignment, which take a CU 49 cycles each
-// where aligned ones take 26 (512 k of a tile 1.5 and 0.8 us): 777 x 1003 x 2005 12.0
-// us, with rows of whole words 10.3.  Whole words around each chunk, shifted in
-// registers, cost as much (12.2, and 12.3 for whole words).  Two or three steps
-// ahead: 1.03 and 1.13 times the time of one.
+// where aligned ones take 26 (512 k of a tile 1.5 and 0.8 us): 777 x 1003 x 2005 12.7
+// us, with rows of whole words (K = 2004) 11.2.  Whole words around each chunk, shifted
+// in registers, cost as much (1.02 times the time, and 1.2 times for whole words).  Two
+// or three steps ahead: 1.03 and 1.13 times the time of one.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -72,7 +72,7 @@ __global__ __launch_bounds__(KG * kThreads) void i8_any_kernel(I8RowsArgs a, Ord
     }
     // A chunk that K cuts is the row's last 16 bytes, moved down when it is staged;
     // one past K is those, moved out.  (Loads under a condition would wait for one
-    // another: 16.6 us in place of 13.7 at 777 x 1003 x 2005.)
+    // another: 1.2 times the time at 777 x 1003 x 2005.)
     u32x4 reg[2][kLoads];
     auto load = [&](int k0) {
         if (K >= 16) {
@@ -190,13 +190,13 @@ hipError_t launch(const I8RowsArgs& a, int out, int xcds, hipStream_t stream) {
 }  // namespace
 
 // us of 64 x 64 tiles with four groups and with one, and of 128 x 128, rows at any byte:
-//   1000 x 1000 x 1000   8.5, 8.2, 18.9   (256 of the small tiles, 64 of the large)
-//   777 x 1003 x 2005    12.6, 13.8, 30   (208, 56)
-//   300 x 4097 x 4095    36, 29, 47       (325, 99)
-//   20000 x 100 x 4095   51, 42.5, 44.9   (626, 157)
-//   128 x 28001 x 4095   88, 78, 54       (876, 219)
-//   4096 x 4097 x 4095   280, 220, 176    (4160, 1056)
-//   5000 x 5000 x 300    132, 52, 57      (6241, 1600)
+//   1000 x 1000 x 1000   7.9, 7.8, 17.0   (256 of the small tiles, 64 of the large)
+//   777 x 1003 x 2005    12.7, 14.0, 30   (208, 56)
+//   300 x 4097 x 4095    36, 30, 47       (325, 99)
+//   20000 x 100 x 4095   53, 45, 45       (626, 157)
+//   128 x 28001 x 4095   90, 79, 55       (876, 219)
+//   4096 x 4097 x 4095   282, 222, 176    (4160, 1056)
+//   5000 x 5000 x 300    123, 44, 53      (6241, 1600)
 int i8_any_tile(int64_t M, int64_t N, int cus) {
     return 4 * ((M + 127) / 128) * ((N + 127) / 128) < 3 * static_cast<int64_t>(cus) ? 64 : 128;
 }

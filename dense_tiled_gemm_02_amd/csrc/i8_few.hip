@@ -1,6 +1,6 @@
 // int8 products with scales where 64 x 64 tiles would leave most of the card
 // empty: few rows (a token to a decode batch), or little of everything.
-// Y = (X W^T) sx sw + b, bound by streaming W: 16 x 8192 x 8192 13.4 us, 5.0 TB/s.
+// Y = (X W^T) sx sw + b, bound by streaming W: 16 x 8192 x 8192 12.6 us, 5.3 TB/s.
 //
 // A workgroup owns 16 NB columns of 16 MB rows; its WV waves take the units of
 // KB k in turn.  Each wave brings its units of W (16 NB rows) and of X through a
@@ -162,11 +162,11 @@ hipError_t launch(const I8RowsArgs& a, hipStream_t stream) {
      "i8_few_kernel<" DTG_STR(MB) "," DTG_STR(NB) "," DTG_STR(KB) "," DTG_STR(ST) "," DTG_STR(XI) "," DTG_STR(WV) ">"}
 
 // Waves, stages and runs by measurement over 12 shapes, W from memory (us):
-//   16 x 16   16 waves, 2 stages  1 x 4096 x 4096 5.7 (4 waves, 6 stages of 128: 6.1)
-//   16 x 32   4 waves, 3 stages   16 x 8192 x 8192 13.4 (8 waves, 2 stages: 15.9)
-//   16 x 64   4 waves, 3 stages   16 x 11008 x 4096 11.7 (8 waves, 2 stages: 12.2)
-//   32 x 32   4 waves, 2 stages   32 x 8192 x 8192 14.0 (8 waves, 2 stages: 16.7)
-//   32 x 64, 64 x 32  the same    32 x 14336 x 4096 13.2, 64 x 8192 x 8192 17.8
+//   16 x 16   16 waves, 2 stages  1 x 4096 x 4096 5.7 (4 waves, 6 stages of 128: 6.2)
+//   16 x 32   4 waves, 3 stages   16 x 8192 x 8192 12.6 (8 waves, 2 stages: 15.9)
+//   16 x 64   4 waves, 3 stages   16 x 11008 x 4096 10.8 (8 waves, 2 stages: 11.0)
+//   32 x 32   4 waves, 2 stages   32 x 8192 x 8192 14.1 (8 waves, 2 stages: 17.1)
+//   32 x 64, 64 x 32  the same    32 x 14336 x 4096 13.3, 64 x 8192 x 8192 18.0
 const I8FewEntry kTable[] = {
     FEW(1, 1, 128, 2, 2, 16),
     FEW(1, 2, 128, 3, 2, 4),

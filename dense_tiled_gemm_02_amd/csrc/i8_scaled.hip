@@ -1,7 +1,8 @@
 // The int8 tile kernel (gemm_dma_kernel.h) with a scale for each row of X and
 // row of W: the same ring and contraction as GEMM_I8's, the sums scaled and
 // rounded in registers and stored as 16-byte chunks of rows.  Bound by the matrix
-// units: 4096 x 14336 x 4096 188 to 199 us (2.4 to 2.6 POP/s), 8192^3 431 us (2.55).
+// units and the clock that they leave: 4096 x 14336 x 4096 190 to 200 us of a layer's
+// values (2.4 to 2.5 POP/s), 213 to 247 of uniform ones; 8192^3 464 us of those (2.4).
 #include "gemm_dma_kernel.h"
 
 namespace dtg {

@@ -10,7 +10,7 @@
 // bits), with the sums across them through the wave's lanes and, where a row
 // takes more than a wave, one LDS word per wave and one barrier.  Bound by memory:
 // x, r are read and y or q (and h) are written once (8192 x 4096 with a residual 45
-// us, 6.0 TB/s; into int8 45; 4096 x 14336 into int8 alone 29).  Rows longer than the
+// us, 5.9 TB/s; into int8 46; 4096 x 14336 into int8 alone 33).  Rows longer than the
 // registers hold are read again for each pass (C = 0); kMaxRow keeps their sums
 // (a chunk's 8, then up to 2048 chunks a thread, in a row) within 2^-13.
 //
@@ -496,14 +496,14 @@ __global__ __launch_bounds__(64 * kSumWaves) void norm_weight_grad_kernel(const 
 // Threads and chunks of 8 to a row of K, by measurement (us of quantization, norm
 // with residual, the same into int8; a CU holds 2048 threads, and wants several
 // rows, of which one waits for memory while another is worked on):
-//   8192 x 4096    256 x 2  18, 45, 45    512 x 1  21, 45, 46    256 x 4   18, 50, 67
-//   4096 x 8192    512 x 2  18, 46, 46    256 x 4  17, 48, 52    1024 x 1  25, 50, 49
-//   4096 x 14336   512 x 4  29, 91, 93    256 x 8  30, 100, 125  1024 x 2  32, 93, 100
-//   16384 x 2048   256 x 1  20, 46, 45    64 x 4   17, 48, 50    512 x 1   31, 54, 66
+//   8192 x 4096    256 x 2  21, 45, 46    512 x 1  26, 45, 48    256 x 4   25, 51, 68
+//   4096 x 8192    512 x 2  22, 46, 47    256 x 4  21, 48, 53    1024 x 1  30, 50, 49
+//   4096 x 14336   512 x 4  33, 91, 94    256 x 8  33, 99, 127   1024 x 2  39, 93, 100
+//   16384 x 2048   256 x 1  25, 46, 46    64 x 4   21, 48, 51    512 x 1   37, 54, 70
 // (a copy's rate: 20, 54, 48 us for the first two and the last, 36, 95, 83 for the
 // third).  Few rows want more threads to each:
-//   1 x 4096       512 x 1  2.6, 2.8, 3.5   256 x 2  2.6, 3.3, 4.0
-//   16 x 14336     1024 x 2  3.4, 4.4, 5.5  512 x 4  3.1, 5.4, 6.5
+//   1 x 4096       512 x 1  2.8, 2.8, 3.3   256 x 2  3.0, 3.5, 4.1
+//   16 x 14336     1024 x 2  4.5, 4.4, 5.7  512 x 4  4.5, 5.4, 6.8
 struct Shape {
     int t, c;
 };
@@ -520,7 +520,7 @@ Shape shape_of(int64_t R, int64_t K) {
     return {1024, 0};
 }
 // Of the gradient, whose sums for dw take registers, too: 8192 x 4096 with a
-// residual 52.6 us for 512 x 1 (256 x 2: 56, 1024 x 1: 68; a copy's rate: 54).
+// residual 53.0 us for 512 x 1 (256 x 2: 56, 1024 x 1: 68; a copy's rate: 54).
 Shape grad_shape_of(int64_t K) {
     if (K <= 128) return {16, 1};
     if (K <= 512) return {64, 1};
@@ -582,8 +582,8 @@ hipError_t launch_rows_as(const RowsArgs& a, hipStream_t stream) {
 // Workgroups of the gradient over R rows of K, in one launch.  Each has a part, K floats
 // written and read again, so a workgroup takes four rows and more, down to one
 // workgroup to a CU; up to as many as keep the memory busy (1024 x 4096: 256 parts
-// 15.5 us, 512 17.1; 8192 x 4096: 52.6 with 512, 1024 63.6; 16384 x 1024: 768 30.2,
-// 1024 31.6).
+// 15.6 us, 512 17.2; 8192 x 4096: 53.0 with 512, 1024 63.6; 16384 x 1024: 768 30.3,
+// 1024 31.5).
 int64_t grad_rows(Shape s) { return s.t < 256 ? 256 / s.t : 1; }
 int64_t most_groups(Shape s) { return s.t >= 1024 ? 256 : s.t == 512 ? 512 : s.t == 64 ? 768 : 1024; }
 int64_t grad_groups(Shape s, int64_t R) {

@@ -14,10 +14,11 @@
 // the ids in order.  16 lanes where 16 logits each are enough: a round's maximum is
 // then four moves inside a quarter wave, and a wave has four rows under way.
 //
-// Bound by instructions, not by bytes: 16384 x 256 in bf16, top 8, 8.5 us (softmax),
-// 18 us (sigmoid with a bias), 20 us (and the best 4 of 8 groups by their best two);
-// its bytes take 2.  512 experts 12, 28 and 35 us, 64 experts 5 to 9.  The gradient
-// of 16384 x 256 7.3 us, of which its bytes are 3.5.
+// Bound by instructions, not by bytes: 16384 x 256 in bf16, top 8, 8.9 us (softmax),
+// 18.5 us (sigmoid with a bias), 21 us (and the best 4 of 8 groups by their best two);
+// its bytes take 2.  512 experts 13, 30 and 34 us, 64 experts 5 to 11.  The gradient
+// of 16384 x 256 8.8 to 9.4 us, of which its bytes are 3.5: each of a lane's J outputs
+// is compared with every one of the `top` chosen.
 //
 // Which of two experts comes first must not depend on rounding.  fp16 and bf16
 // logits without a bias are compared whole: the scores have the logits' order,
@@ -205,7 +206,7 @@ __device__ __forceinline__ uint32_t score_value(float c, float by_size) {
     return 1 + static_cast<uint32_t>(fminf(fmaxf(fmaf(c * by_size, kScoreHalf, kScoreHalf), 0.0f), 2 * kScoreHalf));
 }
 
-// Descending, by a merge-exchange network on J (a power of two) keys.
+// Descending, by Batcher's merge-exchange network on J (a power of two) keys.
 template <int J>
 __device__ __forceinline__ void sort_keys(uint32_t (&k)[J]) {
 #pragma unroll

@@ -127,7 +127,7 @@ def rms_norm(x, weight, residual=None, eps=1e-6, stream=None):
 def rms_norm_i8(x, weight, residual=None, eps=1e-6, stream=None):
     """rms_norm's values in 8 bits: (q, scale), or (q, scale, h) with a residual.
     q: R x K int8, scale: R float32 as i8.i8_quantize makes them, of the values
-    before any rounding to 16 bits.  No gradients."""
+    before any rounding to 16 bits.  No gradients: h, too, is without one."""
     eps = float(eps)
     if stream is None:
         out = _remembered(NORM_I8, eps, x, weight, residual)

@@ -479,8 +479,11 @@ gemm_status gemm_rms_norm_grad(const gemm_norm_problem* prob, const void* dy, co
  * gemm_rms_norm_i8 make the operands.
  *
  * Any sizes, strides and alignment run.  With K and the row strides multiples of
- * 16 and X and W 16-byte aligned, the direct-to-LDS tiles run (M up to 64: kernels
- * that stream W).  Y may overlap no input.  No workspace; capturable. */
+ * 16 and X and W 16-byte aligned, direct-to-LDS kernels run: those that stream W for
+ * up to 32 rows and wherever tiles of at most 64 x 32 outputs fit the device's CUs
+ * in one round, larger tiles else (and where rows lie so far apart that a tile of
+ * them passes 2^31 bytes, the kernel for any alignment).  Y may overlap no input.
+ * No workspace; capturable. */
 typedef struct gemm_i8_problem {
     int64_t M, N, K;            /* M, N up to 2^27 and M N up to 2^35; K below 2^17 */
     int64_t sx, sw;             /* row strides of X and W, bytes */
