@@ -21,8 +21,8 @@ def memory():
     torch.cuda.empty_cache()
 
 
-# of K: the threads of the card that take a row each (or, with others, one)
-@pytest.mark.parametrize("K, at_once", [(72, 16384), (700, 3072), (2000, 1024), (4000, 512), (8200, 256), (16400, 256)])
+# of K: about how many rows a launch has under way, as many threads to each column
+@pytest.mark.parametrize("K, at_once", [(72, 16384), (700, 3000), (2000, 1024), (4000, 512), (8200, 256), (16400, 256)])
 def test_equal_terms(K, at_once):
     print("equal terms", K, flush=True)
     R = 2048 * at_once + 5
